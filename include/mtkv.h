@@ -335,6 +335,116 @@ mt_status mt_paged_attn_decode_cascade_append(const mt_paged_attn_args *args,
 mt_status mt_paged_attn_decode_static(const mt_paged_attn_args *args, uint32_t *status,
                                       mt_stream stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit block-scaled cache (e4m3 codes, a scale for each block and head)
+ *
+ * K and V are paged as everywhere in this library (block table, context
+ * lengths, MT_INVALID_BLOCK_ID holes, cells [head][dim]), but a cell holds
+ * one e4m3 code (sign, 4 exponent bits, 3 fraction bits, no infinities; NaN
+ * is 0x7f) per value, and every (physical block, KV head) has a float32
+ * scale of its own for K and one for V: value = code * scale. This format
+ * has no counterpart in the pages; it is this library's own.
+ *
+ * mt_kv_store_f8 writes scales that are powers of two: the least 2^e (e >=
+ * -126) with amax <= 448 * 2^e. When a later row makes a block's scale grow,
+ * the codes the block already holds are re-encoded; with powers of two that
+ * only shifts exponents, so a value loses nothing unless it falls among the
+ * subnormal codes (below 2^-6 of the scale). The reading calls take any
+ * finite scales.
+ */
+
+/* Element type of the dense arrays of these calls (new rows, rows read
+ * back, queries, outputs). */
+typedef enum { MT_F32 = 0, MT_F16 = 1, MT_BF16 = 2 } mt_dtype;
+
+typedef struct {
+  uint8_t *k_pool;             /* device, n_phys_blocks*block_size cells of
+                                  n_kv_heads*head_dim codes, 16-byte aligned      */
+  uint8_t *v_pool;             /* same shape as k_pool                            */
+  float *k_scales;             /* device float32 [n_phys_blocks][n_kv_heads]      */
+  float *v_scales;
+  const int32_t *block_table;  /* device int32 [n_seqs][max_blocks]               */
+  const int32_t *context_lens; /* device int32 [n_seqs]                           */
+  int n_seqs;
+  int n_kv_heads;              /* 1 .. 256                                        */
+  int head_dim;                /* 64, 128 or 256                                  */
+  int block_size;              /* 16 or 32                                        */
+  int max_blocks;
+  int64_t n_phys_blocks;
+} mt_f8_cache;
+
+/* Store rows into the cache, quantising them as they are written.
+ *   k_new, v_new  device [n_tokens][n_kv_heads*head_dim] of `dtype`, 16-byte
+ *                 aligned.
+ *   q_start       device int32 [n_seqs + 1]: sequence s owns rows q_start[s] ..
+ *                 q_start[s+1]-1; its n rows go to its last n positions
+ *                 context_lens[s]-n .. context_lens[s]-1 (as the queries of
+ *                 mt_paged_attn_prefill). Rows outside every sequence are not
+ *                 read.
+ *   status        device uint32 status word, or NULL.
+ * For each block the rows fall into and each KV head, rows of the block that
+ * lie before the call's first position are kept; slots behind the last
+ * position are left as they were. A block that keeps no rows takes its scale
+ * from the new rows alone, else the scale is the larger of the old one and the
+ * one the new rows need, and the kept rows are re-encoded when it grows. A
+ * kept scale that is not a positive finite number counts as 0 (its rows read
+ * 0). Codes round to nearest, ties to even; NaN stays NaN, infinities become
+ * +-448 * scale and take no part in amax. Rows whose block is a hole are
+ * skipped; an id outside [0, n_phys_blocks), more rows than the context
+ * holds, or rows outside [0, n_tokens) are skipped and flagged. A block may
+ * be stored to by one sequence of a call only (copy on write first:
+ * mt_copy_cells moves a block's cells and, with row_bytes = 4*n_kv_heads, its
+ * row of scales). */
+mt_status mt_kv_store_f8(const mt_f8_cache *cache, mt_dtype dtype, const void *k_new,
+                         const void *v_new, const int32_t *q_start, int n_tokens,
+                         uint32_t *status, mt_stream stream);
+
+/* Read rows back: row j of sequence s (rows q_start[s] .. q_start[s+1]-1 of
+ * k_out, v_out, device [n_tokens][n_kv_heads*head_dim] of `dtype`, 16-byte
+ * aligned) is position pos0[s] + j of the cache, or with pos0 == NULL position
+ * context_lens[s] - n + j (the sequence's last n). Each value is the float32
+ * product code * scale rounded once to `dtype`. A position in a hole reads 0;
+ * one outside [0, context_lens[s]) or with a bad block id reads 0 and is
+ * flagged. Rows outside every sequence are left as they were. */
+mt_status mt_kv_load_f8(const mt_f8_cache *cache, mt_dtype dtype, void *k_out, void *v_out,
+                        const int32_t *q_start, const int32_t *pos0, int n_tokens,
+                        uint32_t *status, mt_stream stream);
+
+/* Arguments of attention over the 8-bit cache. */
+typedef struct {
+  mt_f8_cache cache;
+  mt_dtype dtype;         /* of q and out                                            */
+  const void *q;          /* device [n_tokens][n_heads][head_dim], 16-byte aligned   */
+  void *out;              /* same shape and type, 16-byte aligned                    */
+  float *lse;             /* device float32 [n_tokens][n_heads] (natural log) or NULL */
+  const int32_t *q_start; /* prefill: device int32 [n_seqs + 1]; decode: NULL        */
+  const int32_t *spans;   /* device int32 [n_tokens][2] windows [lo, hi), or NULL    */
+  const int32_t *kv_map;  /* device int32 [n_tokens][MT_KV_MAP_MAX_SPANS][2] runs
+                             (start, len), or NULL; at most one of spans / kv_map    */
+  int n_tokens;           /* rows of q; decode: n_seqs                               */
+  int n_heads;            /* a multiple of n_kv_heads, at most 8 times as many       */
+  float scale;            /* softmax scale                                           */
+} mt_f8_attn_args;
+
+/* Workspace bytes of mt_paged_attn_decode_f8 (0 on invalid args). As for the
+ * other attention calls its first 4 bytes are the device status word: zero
+ * them once after allocating; the rest needs no initial value. Queries the
+ * current device. 16-byte aligned. Calls that may overlap on the GPU need
+ * workspaces of their own. */
+size_t mt_paged_attn_decode_f8_workspace_bytes(const mt_f8_attn_args *args);
+
+/* Grouped-query decode attention (one query per sequence) over the 8-bit
+ * cache: the result that mt_paged_attn_decode defines, on the cache's values,
+ * with the same windows, holes and conventions for rows that see nothing
+ * (out 0, lse -infinity). Codes outside the positions read have no influence,
+ * whatever they are.
+ * Arithmetic: codes enter the tensor cores exactly (as f16); q as a high and
+ * a low f16 part (scores to ~2^-22); softmax statistics, sums and scales in
+ * float32; probabilities as a high and a low f16 part for float32 outputs,
+ * as one f16 for 16-bit outputs. */
+mt_status mt_paged_attn_decode_f8(const mt_f8_attn_args *args, void *workspace,
+                                  size_t workspace_bytes, mt_stream stream);
+
 /* order_moves — "KV Cache Design — cells, format, sessions", section 2:
  * upward moves (dst > src) first, top-down (source descending), then
  * downward moves bottom-up (source ascending), so a destination never lands

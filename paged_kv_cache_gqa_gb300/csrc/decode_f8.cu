@@ -1,0 +1,837 @@
+// Grouped-query decode attention over the 8-bit block-scaled cache (e4m3
+// codes, one float32 scale per physical block and KV head).
+//
+// For query head h of sequence s (KV head h / G), over the positions p that
+// the window and the holes leave:
+//   t_p = scale * sum_i q_i c^K_pi * sK(p),  o = sum_p e^{t_p - m} c^V_p sV(p) / l,
+//   l = sum_p e^{t_p - m},  m = max_p t_p,  lse = m + log l
+// with codes c and the scales sK, sV of the block that holds p.
+//
+// Bound: HBM (2 * head_dim bytes a position and KV head against 4 * G *
+// head_dim operations). Design:
+//  * Work is the stream of all (sequence, head group, 16-position step)
+//    units, cut into equal ranges, one per CTA; every CTA derives its range
+//    from the context lengths. A CTA's warps take the KV heads of the same
+//    steps (and, with few KV heads, interleaved steps), so the lines they
+//    read together form whole blocks of the pool.
+//  * A warp computes 16 positions of one KV head with mma.sync.m16n8k16 and
+//    reads every code from global memory once, by 16-byte asynchronous copies
+//    into a shared-memory queue that is private to the lane: a lane copies
+//    exactly the bytes it uses, so neither barriers nor bank conflicts nor
+//    shuffles come between memory and the matrix instructions.
+//      S = Q K^T: rows 0..7 of A are the high f16 parts of the group's
+//      queries, rows 8..15 the low parts. The k index of the product may run
+//      over the dims in any order, so k step j of lane group c stands for
+//      dims 16c + 4j .. + 3: a lane's 16 bytes of a row are four k steps.
+//      O^T += V^T P^T: rows g and g + 8 of A stand for dims 2m and 2m + 1 of
+//      16g .. 16g + 15 in tile m, so a lane's 16 bytes of a row are its rows
+//      of eight tiles; two positions' bytes pair by byte permutes; P comes
+//      from the lane's own scores.
+//  * Codes become f16 by one conversion per pair (exact). sK multiplies the
+//    scores. sV multiplies the probabilities, relative to the largest sV so
+//    far: the accumulators are kept in units of that largest scale and the
+//    probabilities carry a factor 2^7, so that with the lazy rescaling
+//    (running maximum up to 2^8 behind) their f16 stay below 2^15 and a
+//    probability of 1 has 2^31 steps below it.
+//  * Partial results of a (CTA, sequence, head group) are merged by a second
+//    kernel, a CTA per (sequence, query head).
+#include <limits.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "f8.cuh"
+#include "f8.h"
+#include "mma.cuh"
+
+namespace mtkv {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStep = 16;           // positions of a step
+constexpr int kMaxG = 8;            // query heads per KV head
+constexpr int kMeta = 64;           // step records per warp: two batches of 32
+constexpr int kMinSteps = 8;        // steps of a CTA's range, at least
+constexpr int kHdrBytes = 256;      // status word and padding at the workspace's start
+
+struct DecodeParams {
+  const uint8_t *k_pool, *v_pool;
+  const float *k_scales, *v_scales;
+  const int32_t *table, *ctx, *spans, *kv_map;
+  const void *q;
+  void *out;
+  float *lse;
+  float *part_o;   // [slot][head of the group][D]
+  float2 *part_ml;  // [slot][head of the group]
+  uint32_t *status;
+  int B, Hq, H, G, max_blocks, bs_shift;
+  int hc, n_hg;      // KV heads of a head group, head groups
+  int slices;        // warps that share a KV head's steps
+  int whole;         // 1: CTA i takes all steps of (sequence, head group) i
+  int n_ctas;
+  long long n_phys;
+  float qscale;      // softmax scale * log2(e)
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int KP = D >= 64 ? D / 64 : 1;  // 16-byte K pieces per 8 positions
+  static constexpr int VB = D / 8 < 16 ? D / 8 : 16;  // bytes of a V piece
+  static constexpr int VP = D / 8 / VB;            // V pieces per position of a lane
+  static constexpr int KS = D / 16;                // k steps of Q K^T
+  static constexpr int MT = D / 16;                // dim tiles of O
+  static constexpr int STAGE = 2 * kStep * D;      // bytes of a step's K and V
+  static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr int CTAS = D == 256 ? 1 : 2;    // per SM
+  static constexpr int SMEM = kWarps * (STAGES * STAGE + kMeta * 16);
+};
+
+struct Meta {
+  int phys;       // physical block, or -1
+  uint32_t mask;  // positions of the step that are read
+  float ks, vs;
+};
+
+// Window [lo, hi) of sequence s, empty as (0, 0); with kv_map the span of its runs.
+__device__ __forceinline__ void window(const DecodeParams &p, int s, int &lo, int &hi) {
+  const int cmax = p.max_blocks << p.bs_shift;
+  int c = p.ctx[s];
+  if (c < 0 || c > cmax) {
+    report(p.status, MT_STATUS_BIT_DEVICE_CHECK);
+    c = c < 0 ? 0 : cmax;
+  }
+  lo = 0;
+  hi = c;
+  if (p.spans) {
+    lo = max(p.spans[2 * s], 0);
+    hi = min(p.spans[2 * s + 1], c);
+  } else if (p.kv_map) {
+    lo = INT_MAX;
+    hi = 0;
+#pragma unroll
+    for (int r = 0; r < MT_KV_MAP_MAX_SPANS; ++r) {
+      const int32_t *run = p.kv_map + ((size_t)s * MT_KV_MAP_MAX_SPANS + r) * 2;
+      const int a = max(run[0], 0);
+      const int e = (int)min((long long)run[0] + run[1], (long long)c);
+      if (run[1] > 0 && e > a) {
+        lo = min(lo, a);
+        hi = max(hi, e);
+      }
+    }
+  }
+  if (hi <= lo) lo = hi = 0;
+}
+
+__device__ __forceinline__ int steps_of(int lo, int hi) {
+  return hi > lo ? (hi - 1) / kStep - lo / kStep + 1 : 0;
+}
+
+// Steps of all sequences before s, and of all sequences: the whole warp takes part.
+__device__ __forceinline__ void count_steps(const DecodeParams &p, int s, long long &before,
+                                            long long &total) {
+  const int lane = threadIdx.x & 31;
+  before = total = 0;
+  for (int t = lane; t < p.B; t += 32) {
+    int lo, hi;
+    window(p, t, lo, hi);
+    const int n = steps_of(lo, hi);
+    total += n;
+    if (t < s) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(kAll, before, o);
+    total += __shfl_xor_sync(kAll, total, o);
+  }
+}
+
+// CTAs that a launch's ranges use: none with less than kMinSteps of work.
+__device__ __forceinline__ int ctas_used(const DecodeParams &p, long long total) {
+  return (int)max(1LL, min((long long)p.n_ctas, total / kMinSteps));
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool ok) {
+  const int n = ok ? BYTES : 0;  // 0: nothing is read, the destination is zero-filled
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 4 consecutive dense elements as floats.
+template <int DT>
+__device__ __forceinline__ float4 load4(const void *p, size_t i) {
+  if constexpr (DT == MT_F32) {
+    return __ldg(reinterpret_cast<const float4 *>(p) + i / 4);
+  } else {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p) + i / 4);
+    if constexpr (DT == MT_F16) {
+      const float2 a = h2_to_f2(w.x), b = h2_to_f2(w.y);
+      return make_float4(a.x, a.y, b.x, b.y);
+    } else {
+      return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                         __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+    }
+  }
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
+    decode_f8_kernel(const __grid_constant__ DecodeParams p) {
+  using C = Cfg<D>;
+  constexpr int ST = C::STAGES;
+  constexpr bool PLO = DT == MT_F32;  // low parts of the probabilities too
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  uint8_t *ring = smem + warp * (ST * C::STAGE);
+  Meta *meta = reinterpret_cast<Meta *>(smem + kWarps * ST * C::STAGE) + warp * kMeta;
+  const uint32_t ring_a = smem_u32(ring);
+  pdl_enter();
+
+  // ---- this CTA's range of the stream (sequence, head group, step)
+  long long r0 = 0, r1 = 0;
+  int s = 0, hg = 0;       // where it starts
+  long long skip = 0;      // steps of (s, hg) before the range
+  if (p.whole) {
+    s = blockIdx.x / p.n_hg;
+    hg = blockIdx.x % p.n_hg;
+    r1 = INT_MAX;
+  } else {
+    long long before, total;
+    count_steps(p, 0, before, total);
+    total *= p.n_hg;
+    const int n = ctas_used(p, total);
+    if ((int)blockIdx.x >= n) return;
+    r0 = total * blockIdx.x / n;
+    r1 = total * (blockIdx.x + 1) / n;
+    if (r0 >= r1) return;
+    // the sequence that holds unit r0: prefix sums of 32 sequences at a time
+    long long run = 0;
+    for (int b0 = 0;; b0 += 32) {
+      int k = 0;
+      if (b0 + lane < p.B) {
+        int lo, hi;
+        window(p, b0 + lane, lo, hi);
+        k = steps_of(lo, hi);
+      }
+      long long incl = (long long)k * p.n_hg;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t past = __ballot_sync(kAll, run + incl > r0);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        s = b0 + l;
+        const int ks = __shfl_sync(kAll, k, l);
+        const long long off = r0 - (run + __shfl_sync(kAll, incl, l) - (long long)ks * p.n_hg);
+        hg = (int)(off / ks);
+        skip = off % ks;
+        break;
+      }
+      run += __shfl_sync(kAll, incl, 31);
+    }
+  }
+
+  long long left = r1 - r0;
+  const int head_l = warp % p.hc, slice = warp / p.hc;  // within the head group
+  int slot_cta = blockIdx.x;
+  while (left > 0 && s < p.B) {
+    // ---- a segment: steps [a, b) of (s, hg)
+    int lo, hi;
+    window(p, s, lo, hi);
+    const int n_all = steps_of(lo, hi);
+    const int a = (int)skip;
+    const int b = (int)min((long long)n_all, skip + left);
+    const int kvh = hg * p.hc + head_l;
+    const bool mine = slice < p.slices && kvh < p.H;
+    const int n_mine = mine && a + slice < b ? (b - a - slice + p.slices - 1) / p.slices : 0;
+    const int step0 = lo / kStep + a + slice;
+
+    float oacc[C::MT][4];
+#pragma unroll
+    for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) oacc[m][i] = 0.f;
+    float m_run = -INFINITY, l_run = 0.f, v_ref = 0.f;
+
+    if (n_mine > 0) {
+      // ---- step records: id, mask and scales of 32 steps at a time, a batch
+      // ahead: ids 32 steps before their use, scales 16 before
+      const int bps = p.bs_shift == 5 ? 1 : 0;
+      auto fetch_id = [&](int k) -> int {  // of this warp's step k
+        if (k >= n_mine) return -1;
+        const int blk = (step0 + k * p.slices) >> bps;
+        return p.table[(size_t)s * p.max_blocks + blk];
+      };
+      auto check_id = [&](int &id) {
+        if (id < -1 || (long long)id >= p.n_phys) {
+          report(p.status, MT_STATUS_BIT_DEVICE_CHECK);
+          id = -1;
+        }
+      };
+      auto mask_of = [&](int k, int id) -> uint32_t {
+        if (id < 0) return 0u;
+        const int pos = (step0 + k * p.slices) * kStep;
+        auto bits = [&](int x, int y) -> uint32_t {  // positions [x, y)
+          x = max(x - pos, 0);
+          y = min(y - pos, kStep);
+          return y > x ? ((1u << y) - 1u) & ~((1u << x) - 1u) : 0u;
+        };
+        if (!p.kv_map) return bits(lo, hi);
+        uint32_t m = 0;
+        for (int r = 0; r < MT_KV_MAP_MAX_SPANS; ++r) {
+          const int32_t *run = p.kv_map + ((size_t)s * MT_KV_MAP_MAX_SPANS + r) * 2;
+          if (run[1] > 0)
+            m |= bits(max(run[0], 0), (int)min((long long)run[0] + run[1], (long long)hi));
+        }
+        return m;
+      };
+      auto put = [&](int k, int id, float ks, float vs) {
+        meta[k & (kMeta - 1)] = Meta{id, mask_of(k, id), ks, vs};
+      };
+      auto scale_of = [&](const float *sc, int id) -> float {
+        return id >= 0 ? __ldg(sc + (size_t)id * p.H + kvh) : 0.f;
+      };
+      int id_n = fetch_id(lane);
+      check_id(id_n);
+      put(lane, id_n, scale_of(p.k_scales, id_n), scale_of(p.v_scales, id_n));
+      id_n = fetch_id(32 + lane);
+      float ks_n = 0.f, vs_n = 0.f;
+      __syncwarp();
+
+      // ---- the copies of step k into its queue slot
+      const size_t row = (size_t)p.H * D;
+      auto issue = [&](int k) {
+        if (k < n_mine) {
+          const Meta &mt = meta[k & (kMeta - 1)];
+          const uint32_t mask = mt.mask;
+          const uint32_t dst = ring_a + (uint32_t)(k % ST) * C::STAGE;
+          const int half = p.bs_shift == 5 ? ((step0 + k * p.slices) & 1) * kStep : 0;
+          const size_t base = (((size_t)max(mt.phys, 0) << p.bs_shift) + half) * row + (size_t)kvh * D;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int r = 8 * t + g;
+            const bool ok = (mask >> r) & 1u;
+            const uint8_t *src = p.k_pool + base + (size_t)r * row + 16 * c;
+#pragma unroll
+            for (int j = 0; j < C::KP; ++j)
+              copy_async<16>(dst + (t * C::KP + j) * 512 + lane * 16, ok ? src + 64 * j : p.k_pool,
+                             ok);
+          }
+          const uint32_t vdst = dst + kStep * D;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int r = 2 * c + (t & 1) + 8 * (t >> 1);
+            const bool ok = (mask >> r) & 1u;
+            const uint8_t *src = p.v_pool + base + (size_t)r * row + C::VB * g;
+#pragma unroll
+            for (int j = 0; j < C::VP; ++j)
+              copy_async<C::VB>(vdst + (t * C::VP + j) * (32 * C::VB) + lane * C::VB,
+                                ok ? src + 128 * j : p.v_pool, ok);
+          }
+        }
+        copy_commit();
+      };
+#pragma unroll
+      for (int k = 0; k < ST - 1; ++k) issue(k);
+
+      // ---- the group's queries as A fragments: q / 2^e in high and low f16
+      // parts, 2^e bringing the row's largest value to [2^11, 2^12)
+      uint32_t qa[C::KS][4];
+      float qfac;  // the row's factor on scores, 2^e * scale * log2(e)
+      {
+        const bool row_ok = g < p.G;
+        const size_t qrow =
+            ((size_t)s * p.Hq + (size_t)kvh * p.G + (row_ok ? g : 0)) * D;
+        float qmax = 0.f;
+        float4 x[C::KS];
+#pragma unroll
+        for (int j = 0; j < C::KS; ++j) {
+          const int d = (j >> 2) * 64 + 16 * c + 4 * (j & 3);
+          x[j] = row_ok ? load4<DT>(p.q, qrow + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+          qmax = fmaxf(fmaxf(qmax, fmaxf(fabsf(x[j].x), fabsf(x[j].y))),
+                       fmaxf(fabsf(x[j].z), fabsf(x[j].w)));
+        }
+        qmax = fmaxf(qmax, __shfl_xor_sync(kAll, qmax, 1));
+        qmax = fmaxf(qmax, __shfl_xor_sync(kAll, qmax, 2));
+        // f = 2^(138 - exponent field), so qmax * f lies in [2^11, 2^12); its
+        // own exponent kept within the normal range
+        const int ef = (int)(__float_as_uint(qmax) >> 23);
+        const int fe = min(max(265 - ef, 1), 253);
+        const float f = qmax > 0.f ? __uint_as_float((uint32_t)fe << 23) : 1.f;
+        qfac = p.qscale / f;
+#pragma unroll
+        for (int j = 0; j < C::KS; ++j) {
+          split_h2(x[j].x * f, x[j].y * f, qa[j][0], qa[j][1]);
+          split_h2(x[j].z * f, x[j].w * f, qa[j][2], qa[j][3]);
+        }
+      }
+
+      for (int k = 0; k < n_mine; ++k) {
+        const int ki = k + ST - 1;  // the step whose copies start now
+        if ((ki & 31) == 16) {
+          check_id(id_n);
+          ks_n = scale_of(p.k_scales, id_n);
+          vs_n = scale_of(p.v_scales, id_n);
+        } else if ((ki & 31) == 31) {
+          const int k0 = (ki & ~31) + 32;
+          if (k0 < n_mine) {
+            put(k0 + lane, id_n, ks_n, vs_n);
+            id_n = fetch_id(k0 + 32 + lane);
+          }
+          __syncwarp();
+        }
+        issue(ki);
+        copy_wait<ST - 1>();
+        const Meta mt = meta[k & (kMeta - 1)];
+        if (mt.mask == 0u) continue;
+        const uint32_t st = ring_a + (uint32_t)(k % ST) * C::STAGE;
+
+        // ---- scores
+        float sc[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < C::KP; ++j) {
+            const uint4 w = lds16(st + (t * C::KP + j) * 512 + lane * 16);
+            uint32_t b0, b1;
+            f8::code4_to_h2(w.x, b0, b1);
+            mma_f16(s0, qa[4 * j], b0, b1);
+            f8::code4_to_h2(w.y, b0, b1);
+            mma_f16(s1, qa[4 * j + 1], b0, b1);
+            f8::code4_to_h2(w.z, b0, b1);
+            mma_f16(s0, qa[4 * j + 2], b0, b1);
+            f8::code4_to_h2(w.w, b0, b1);
+            mma_f16(s1, qa[4 * j + 3], b0, b1);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[t][i] = s0[i] + s1[i];
+        }
+        // head g's scores at positions 2c, 2c + 1, 8 + 2c, 9 + 2c
+        const float f = qfac * mt.ks;
+        float x[4] = {(sc[0][0] + sc[0][2]) * f, (sc[0][1] + sc[0][3]) * f,
+                      (sc[1][0] + sc[1][2]) * f, (sc[1][1] + sc[1][3]) * f};
+        if (mt.mask != 0xffffu) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+            if (!((mt.mask >> r) & 1u)) x[i] = -INFINITY;
+          }
+        }
+        // ---- running maximum: rescaled only when a row grows past 2^8 (or
+        // has its first position) or a larger V scale comes
+        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        if (__any_sync(kAll, mx > m_run + 8.f || (m_run == -INFINITY && mx != -INFINITY) ||
+                                 mt.vs > v_ref)) {
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
+          const float m_new = fmaxf(m_run, mx);
+          float al = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
+          m_run = m_new;
+          l_run *= al;
+          const float v_new = fmaxf(v_ref, mt.vs);
+          al *= v_new > 0.f ? v_ref / v_new : 1.f;
+          v_ref = v_new;
+          const float a0 = __shfl_sync(kAll, al, 8 * c), a1 = __shfl_sync(kAll, al, 8 * c + 4);
+#pragma unroll
+          for (int m = 0; m < C::MT; ++m) {
+            oacc[m][0] *= a0;
+            oacc[m][1] *= a1;
+            oacc[m][2] *= a0;
+            oacc[m][3] *= a1;
+          }
+        }
+        // ---- probabilities
+        const float mr = m_run == -INFINITY ? 0.f : m_run;
+        const float wv = v_ref > 0.f ? 128.f * (mt.vs / v_ref) : 0.f;
+        float pr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pr[i] = ex2(x[i] - mr);
+          l_run += pr[i];
+          pr[i] *= wv;
+        }
+        uint32_t ph[2], pl[2];
+        split_h2(pr[0], pr[1], ph[0], pl[0]);
+        split_h2(pr[2], pr[3], ph[1], pl[1]);
+        // ---- O^T += V^T P^T
+        const uint32_t vt = st + kStep * D;
+#pragma unroll
+        for (int j = 0; j < C::VP; ++j) {
+          uint32_t w[4][C::VB / 4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t at = vt + (t * C::VP + j) * (32 * C::VB) + lane * C::VB;
+            if constexpr (C::VB == 16) {
+              const uint4 u = lds16(at);
+              w[t][0] = u.x;
+              w[t][1] = u.y;
+              w[t][2] = u.z;
+              w[t][3] = u.w;
+            } else {
+              const uint2 u = lds8(at);
+              w[t][0] = u.x;
+              w[t][1] = u.y;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < C::VB / 4; ++i) {
+            uint32_t a0[4], a1[4];
+            f8::code4_to_h2(__byte_perm(w[0][i], w[1][i], 0x5140), a0[0], a0[1]);
+            f8::code4_to_h2(__byte_perm(w[2][i], w[3][i], 0x5140), a0[2], a0[3]);
+            f8::code4_to_h2(__byte_perm(w[0][i], w[1][i], 0x7362), a1[0], a1[1]);
+            f8::code4_to_h2(__byte_perm(w[2][i], w[3][i], 0x7362), a1[2], a1[3]);
+            const int m = j * 8 + 2 * i;
+            mma_f16(oacc[m], a0, ph[0], ph[1]);
+            mma_f16(oacc[m + 1], a1, ph[0], ph[1]);
+            if constexpr (PLO) {
+              mma_f16(oacc[m], a0, pl[0], pl[1]);
+              mma_f16(oacc[m + 1], a1, pl[0], pl[1]);
+            }
+          }
+        }
+      }
+      copy_wait<0>();
+      l_run += __shfl_xor_sync(kAll, l_run, 1);
+      l_run += __shfl_xor_sync(kAll, l_run, 2);
+    }
+
+    // ---- the accumulators in units of 1, relative to m
+    {
+      const float u = v_ref * (1.f / 128.f);
+#pragma unroll
+      for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) oacc[m][i] *= u;
+    }
+    // ---- warps that shared a KV head's steps: merged by the first of them
+    if (p.slices > 1) {
+      float *own = reinterpret_cast<float *>(ring);  // [8 heads][D], then m[8], l[8] in meta
+      float2 *ml = reinterpret_cast<float2 *>(meta);
+      if (slice > 0) {
+#pragma unroll
+        for (int m = 0; m < C::MT; ++m) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) own[(m * 4 + i) * 32 + lane] = oacc[m][i];
+        }
+        if (c == 0) ml[g] = make_float2(m_run, l_run);
+      }
+      __syncthreads();
+      if (slice == 0 && mine) {
+        for (int w = 1; w < p.slices; ++w) {
+          const int ow = warp + w * p.hc;
+          const float *oo = reinterpret_cast<const float *>(smem + ow * (ST * C::STAGE));
+          const float2 o_ml = reinterpret_cast<const float2 *>(
+              smem + kWarps * ST * C::STAGE + (size_t)ow * kMeta * sizeof(Meta))[g];
+          if (__any_sync(kAll, o_ml.x != -INFINITY || o_ml.y != 0.f)) {
+            const float m_new = fmaxf(m_run, o_ml.x);
+            const float f0 = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
+            const float f1 = o_ml.x == -INFINITY ? 0.f : ex2(o_ml.x - m_new);
+            l_run = l_run * f0 + o_ml.y * f1;
+            m_run = m_new;
+            const float x0 = __shfl_sync(kAll, f0, 8 * c), x1 = __shfl_sync(kAll, f0, 8 * c + 4);
+            const float y0 = __shfl_sync(kAll, f1, 8 * c), y1 = __shfl_sync(kAll, f1, 8 * c + 4);
+#pragma unroll
+            for (int m = 0; m < C::MT; ++m) {
+              const float *ov = oo + m * 128 + lane;
+              oacc[m][0] = oacc[m][0] * x0 + ov[0] * y0;
+              oacc[m][1] = oacc[m][1] * x1 + ov[32] * y1;
+              oacc[m][2] = oacc[m][2] * x0 + ov[64] * y0;
+              oacc[m][3] = oacc[m][3] * x1 + ov[96] * y1;
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    // ---- heads 2c and 2c + 1: dims 16 g + 2 m + (0, 1) of each 128-dim part
+    if (mine && slice == 0) {
+      const bool done = a == 0 && b == n_all;  // the whole (sequence, head group)
+      const float l0 = __shfl_sync(kAll, l_run, 8 * c), l1 = __shfl_sync(kAll, l_run, 8 * c + 4);
+      const size_t slot = (size_t)slot_cta + (size_t)s * p.n_hg + hg;
+      constexpr int SPAN = C::VB;  // consecutive dims of a lane
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hd = 2 * c + e;
+        if (hd >= p.G) continue;
+        const float l = e ? l1 : l0;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t orow = ((size_t)s * p.Hq + (size_t)kvh * p.G + hd) * D;
+        float *prow = p.part_o + (slot * (p.hc * p.G) + head_l * p.G + hd) * D;
+#pragma unroll
+        for (int m = 0; m < C::MT; m += 2) {
+          const int d = (m * 2 / SPAN) * 128 + SPAN * g + (m * 2) % SPAN;
+          const float v0 = oacc[m][e], v1 = oacc[m][2 + e], v2 = oacc[m + 1][e],
+                      v3 = oacc[m + 1][2 + e];
+          if (done)
+            f8::store4<DT>(p.out, orow + d, v0 * inv, v1 * inv, v2 * inv, v3 * inv);
+          else
+            f8::store4<MT_F32>(prow, d, v0, v1, v2, v3);
+        }
+      }
+      if (c == 0 && g < p.G) {
+        if (!done)
+          p.part_ml[slot * (p.hc * p.G) + head_l * p.G + g] = make_float2(m_run, l_run);
+        else if (p.lse)
+          p.lse[(size_t)s * p.Hq + (size_t)kvh * p.G + g] =
+              l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994530942f;
+      }
+    }
+    if (p.whole) break;
+    left -= b - a;
+    skip = 0;
+    if (++hg == p.n_hg) {
+      hg = 0;
+      // the next sequence with work
+      do {
+        ++s;
+        if (s >= p.B) break;
+        window(p, s, lo, hi);
+      } while (hi <= lo);
+    }
+  }
+}
+
+// Merge the partial results of split (sequence, head group)s, a CTA per
+// (sequence, query head): warps take the pieces in turn, then merge through
+// shared memory. Sequences that see nothing get 0 and -infinity here; those
+// that one CTA finished are left alone.
+constexpr int kMergeWarps = 4;
+
+template <int D, int DT>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    merge_f8_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int DV = D / 32;
+  __shared__ float o_s[kMergeWarps][D];
+  __shared__ float2 ml_s[kMergeWarps];
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+  const int kvh = h / p.G, hg = kvh / p.hc;
+  // lengths and windows are inputs: read before the decode kernel has ended
+  long long before, total;
+  count_steps(p, s, before, total);
+  int lo, hi;
+  window(p, s, lo, hi);
+  const int n_all = steps_of(lo, hi);
+  int c0 = 0, c1 = -1;  // CTAs that hold pieces
+  if (n_all > 0) {
+    total *= p.n_hg;
+    const int n = ctas_used(p, total);
+    const long long u0 = before * p.n_hg + (long long)hg * n_all, u1 = u0 + n_all - 1;
+    // CTA i holds units [total i / n, total (i + 1) / n)
+    c0 = (int)(((u0 + 1) * n - 1) / total);
+    c1 = (int)(((u1 + 1) * n - 1) / total);
+  }
+  // every CTA waits, also one with nothing to merge: this grid must not
+  // complete before the decode has, or the stream's next kernel could start
+  pdl_wait();
+  if (c0 == c1) return;
+  const int hin = (kvh - hg * p.hc) * p.G + h % p.G, per = p.hc * p.G;
+  float M = -INFINITY, L = 0.f, acc[DV];
+#pragma unroll
+  for (int e = 0; e < DV; ++e) acc[e] = 0.f;
+  const size_t slot0 = (size_t)s * p.n_hg + hg;
+#pragma unroll 4
+  for (int i = c0 + warp; i <= c1; i += kMergeWarps) {
+    const size_t rec = (slot0 + i) * per + hin;
+    const float2 ml = __ldcg(p.part_ml + rec);
+    float v[DV];
+#pragma unroll
+    for (int e = 0; e < DV; e += 2) {
+      const float2 x = __ldcg(reinterpret_cast<const float2 *>(p.part_o + rec * D + lane * DV + e));
+      v[e] = x.x;
+      v[e + 1] = x.y;
+    }
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // a piece that saw nothing
+    const float m_new = fmaxf(M, ml.x);
+    const float f0 = M == -INFINITY ? 0.f : ex2(M - m_new), f1 = ex2(ml.x - m_new);
+    M = m_new;
+    L = L * f0 + ml.y * f1;
+#pragma unroll
+    for (int e = 0; e < DV; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
+  }
+  if (lane == 0) ml_s[warp] = make_float2(M, L);
+#pragma unroll
+  for (int e = 0; e < DV; ++e) o_s[warp][lane * DV + e] = acc[e];
+  __syncthreads();
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, ml_s[w].x);
+  L = 0.f;
+  float f[kMergeWarps];
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    f[w] = ml_s[w].x == -INFINITY ? (ml_s[w].y == 0.f ? 0.f : 1.f) : ex2(ml_s[w].x - M);
+    L += ml_s[w].y * f[w];
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const size_t orow = ((size_t)s * p.Hq + h) * D;
+  for (int d = threadIdx.x * 4; d < D; d += 128 * kMergeWarps) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += o_s[w][d + e] * f[w];
+    f8::store4<DT>(p.out, orow + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  }
+  if (p.lse && threadIdx.x == 0)
+    p.lse[(size_t)s * p.Hq + h] =
+        L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+}
+
+// --------------------------------------------------------------------- host
+
+struct Plan {
+  DecodeParams p;
+  long long ctas, slots;
+  size_t ws;
+};
+
+mt_status make_plan(const mt_f8_attn_args *a, const char *where, Plan *pl) {
+  const std::string w = std::string(where) + ": ";
+  if (!a) return fail(MT_ERR_INVALID_ARG, w + "null args");
+  mt_status st = check_f8_cache(&a->cache, where);
+  if (st != MT_OK) return st;
+  const mt_f8_cache &c = a->cache;
+  if (!dtype_bytes(a->dtype)) return fail(MT_ERR_INVALID_ARG, w + "unknown dtype");
+  if (a->n_heads <= 0 || a->n_heads % c.n_kv_heads)
+    return fail(MT_ERR_INVALID_ARG, w + "n_heads must be a positive multiple of n_kv_heads");
+  if (a->n_heads / c.n_kv_heads > kMaxG)
+    return fail(MT_ERR_UNSUPPORTED, w + "more than 8 query heads per KV head");
+  if (a->n_tokens != c.n_seqs)
+    return fail(MT_ERR_INVALID_ARG, w + "n_tokens must equal n_seqs");
+  if (a->q_start) return fail(MT_ERR_INVALID_ARG, w + "q_start is for prefill");
+  if (a->spans && a->kv_map)
+    return fail(MT_ERR_INVALID_ARG, w + "at most one of spans and kv_map");
+  if (c.n_seqs > 0 && (!a->q || !a->out)) return fail(MT_ERR_INVALID_ARG, w + "null pointer");
+  if (!aligned16(a->q) || !aligned16(a->out))
+    return fail(MT_ERR_INVALID_ARG, w + "q and out must be 16-byte aligned");
+  if ((long long)c.n_seqs * a->n_heads > 0x7fffffffLL)
+    return fail(MT_ERR_UNSUPPORTED, w + "too many query rows");
+  DeviceInfo di;
+  st = device_info(&di);
+  if (st != MT_OK) return st;
+  DecodeParams &p = pl->p;
+  p = DecodeParams{};
+  p.k_pool = c.k_pool;
+  p.v_pool = c.v_pool;
+  p.k_scales = c.k_scales;
+  p.v_scales = c.v_scales;
+  p.table = c.block_table;
+  p.ctx = c.context_lens;
+  p.spans = a->spans;
+  p.kv_map = a->kv_map;
+  p.q = a->q;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.B = c.n_seqs;
+  p.Hq = a->n_heads;
+  p.H = c.n_kv_heads;
+  p.G = a->n_heads / c.n_kv_heads;
+  p.max_blocks = c.max_blocks;
+  p.bs_shift = c.block_size == 32 ? 5 : 4;
+  p.n_phys = c.n_phys_blocks;
+  p.qscale = a->scale * 1.44269504088896340736f;
+  p.hc = std::min(p.H, kWarps);
+  p.n_hg = (p.H + p.hc - 1) / p.hc;
+  p.slices = kWarps / p.hc;
+  const long long rows = (long long)p.B * p.n_hg;
+  // a (sequence, head group) of up to 256 positions is one CTA's work: no
+  // pieces and no second launch
+  p.whole = (long long)p.max_blocks * c.block_size <= 256 && rows <= 0x7fffffffLL;
+  const int per_sm = c.head_dim == 256 ? 1 : 2;
+  pl->ctas = p.whole ? rows : (long long)per_sm * di.n_sm;
+  p.n_ctas = (int)pl->ctas;
+  pl->slots = p.whole ? 0 : pl->ctas + rows;
+  pl->ws = kHdrBytes + (size_t)pl->slots * p.hc * p.G * (c.head_dim + 2) * sizeof(float);
+  return MT_OK;
+}
+
+template <int D, int DT>
+mt_status launch(const Plan &pl, cudaStream_t s) {
+  auto kern = decode_f8_kernel<D, DT>;
+  constexpr int smem = Cfg<D>::SMEM;
+  mt_status st = kernel_smem(reinterpret_cast<const void *>(kern), smem,
+                             "cudaFuncSetAttribute(f8 decode smem)", true);
+  if (st != MT_OK) return st;
+  st = cuda_check(launch_pdl(kern, dim3((unsigned)pl.ctas), dim3(kThreads), smem, s, pl.p),
+                  "f8 decode launch");
+  if (st != MT_OK || pl.p.whole) return st;
+  return cuda_check(launch_pdl(merge_f8_kernel<D, DT>, dim3((unsigned)(pl.p.B * pl.p.Hq)),
+                               dim3(32 * kMergeWarps), 0, s, pl.p),
+                    "f8 decode merge launch");
+}
+
+template <int D>
+mt_status launch_dt(const Plan &pl, mt_dtype t, cudaStream_t s) {
+  if (t == MT_F32) return launch<D, MT_F32>(pl, s);
+  if (t == MT_F16) return launch<D, MT_F16>(pl, s);
+  return launch<D, MT_BF16>(pl, s);
+}
+
+}  // namespace
+}  // namespace mtkv
+
+using namespace mtkv;
+
+extern "C" size_t mt_paged_attn_decode_f8_workspace_bytes(const mt_f8_attn_args *a) {
+  Plan pl;
+  return make_plan(a, "mt_paged_attn_decode_f8_workspace_bytes", &pl) == MT_OK ? pl.ws : 0;
+}
+
+extern "C" mt_status mt_paged_attn_decode_f8(const mt_f8_attn_args *a, void *workspace,
+                                             size_t workspace_bytes, mt_stream stream) {
+  Plan pl;
+  mt_status st = make_plan(a, "mt_paged_attn_decode_f8", &pl);
+  if (st != MT_OK) return st;
+  if (!workspace || workspace_bytes < pl.ws || !aligned16(workspace))
+    return fail(MT_ERR_INVALID_ARG,
+                "mt_paged_attn_decode_f8: workspace missing, too small or not 16-byte aligned");
+  if (a->cache.n_seqs == 0) return ok();
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  pl.p.status = reinterpret_cast<uint32_t *>(ws);
+  pl.p.part_o = reinterpret_cast<float *>(ws + kHdrBytes);
+  pl.p.part_ml = reinterpret_cast<float2 *>(
+      pl.p.part_o + (size_t)pl.slots * pl.p.hc * pl.p.G * a->cache.head_dim);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = a->cache.head_dim == 64    ? launch_dt<64>(pl, a->dtype, s)
+       : a->cache.head_dim == 128 ? launch_dt<128>(pl, a->dtype, s)
+                                  : launch_dt<256>(pl, a->dtype, s);
+  return st == MT_OK ? ok() : st;
+}

@@ -72,6 +72,27 @@ class mt_paged_attn_args(ctypes.Structure):
                 ("kv_map", ctypes.c_void_p)]
 
 
+MT_F32, MT_F16, MT_BF16 = 0, 1, 2
+_DTYPES = {torch.float32: MT_F32, torch.float16: MT_F16, torch.bfloat16: MT_BF16}
+
+
+class mt_f8_cache(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("block_size", ctypes.c_int),
+                ("max_blocks", ctypes.c_int), ("n_phys_blocks", ctypes.c_int64)]
+
+
+class mt_f8_attn_args(ctypes.Structure):
+    _fields_ = [("cache", mt_f8_cache), ("dtype", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("spans", ctypes.c_void_p),
+                ("kv_map", ctypes.c_void_p), ("n_tokens", ctypes.c_int),
+                ("n_heads", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -101,6 +122,10 @@ def lib() -> ctypes.CDLL:
         "mt_paged_attn_decode_cascade_append": (I, [ctypes.POINTER(mt_paged_attn_args),
                                                     ctypes.POINTER(mt_prefix_group), I, P, P, P,
                                                     SZ, P]),
+        "mt_kv_store_f8": (I, [ctypes.POINTER(mt_f8_cache), I, P, P, P, I, U32P, P]),
+        "mt_kv_load_f8": (I, [ctypes.POINTER(mt_f8_cache), I, P, P, P, P, I, U32P, P]),
+        "mt_paged_attn_decode_f8_workspace_bytes": (SZ, [ctypes.POINTER(mt_f8_attn_args)]),
+        "mt_paged_attn_decode_f8": (I, [ctypes.POINTER(mt_f8_attn_args), P, SZ, P]),
         "mt_order_moves": (I, [ctypes.POINTER(mt_move), I, ctypes.POINTER(I)]),
         "mt_check_moves": (I, [ctypes.POINTER(mt_move), I, I64, ctypes.POINTER(I)]),
         "mt_copy_cells": (I, [ctypes.POINTER(P), I, SZ, I64, ctypes.POINTER(mt_move), I, U32P,
@@ -300,6 +325,122 @@ def mt_paged_attn_decode_static(args: mt_paged_attn_args, status=None, stream=No
     (for callers that cannot allocate device memory when they decode)."""
     _check(lib().mt_paged_attn_decode_static(ctypes.byref(args), _ptr(status), _stream(stream)),
            "mt_paged_attn_decode_static")
+
+
+def _ptr_here(t, dtypes, what: str) -> int | None:
+    """Address of a contiguous tensor of one of `dtypes` on the current device
+    (the calls launch there)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: expected a tensor on the current CUDA device, got {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: unexpected dtype {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def f8_cache(k_pool, v_pool, k_scales, v_scales, block_table, context_lens) -> mt_f8_cache:
+    """Descriptor of an 8-bit block-scaled cache, kept as long as its tensors:
+    pools [n_phys_blocks][block_size][n_kv_heads][head_dim] of e4m3 codes
+    (uint8 or float8_e4m3fn), scales float32 [n_phys_blocks][n_kv_heads],
+    block_table int32 [n_seqs][max_blocks], context_lens int32 [n_seqs]."""
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+        raise ValueError("f8_cache: pools must share one [blocks][block_size][heads][dim] shape")
+    n_phys, bs, hkv, d = k_pool.shape
+    if k_scales.shape != (n_phys, hkv) or v_scales.shape != (n_phys, hkv):
+        raise ValueError("f8_cache: scales must be [blocks][heads]")
+    if block_table.dim() != 2 or context_lens.shape != (block_table.shape[0],):
+        raise ValueError("f8_cache: block_table must be [n_seqs][max_blocks], "
+                         "context_lens [n_seqs]")
+    c = mt_f8_cache()
+    c.k_pool, c.v_pool = _ptr_here(k_pool, _CODES, "k_pool"), _ptr_here(v_pool, _CODES, "v_pool")
+    c.k_scales = _ptr_here(k_scales, _F32, "k_scales")
+    c.v_scales = _ptr_here(v_scales, _F32, "v_scales")
+    c.block_table = _ptr_here(block_table, _I32, "block_table")
+    c.context_lens = _ptr_here(context_lens, _I32, "context_lens")
+    c.n_seqs, c.max_blocks = block_table.shape
+    c.n_kv_heads, c.head_dim, c.block_size, c.n_phys_blocks = hkv, d, bs, n_phys
+    c._tensors = (k_pool, v_pool, k_scales, v_scales, block_table, context_lens)
+    return c
+
+
+def _f8_rows(cache, k, v, q_start, what: str) -> tuple:
+    """dtype, addresses and row count of a pair of dense row arrays."""
+    dt = _DTYPES.get(k.dtype)
+    n = k.shape[0]
+    if dt is None or v.dtype != k.dtype:
+        raise ValueError(f"{what}: rows must be float32, float16 or bfloat16, both alike")
+    if k.shape != v.shape or k.numel() != n * cache.n_kv_heads * cache.head_dim:
+        raise ValueError(f"{what}: rows must be [n_tokens][n_kv_heads][head_dim], both alike")
+    if q_start.shape != (cache.n_seqs + 1,):
+        raise ValueError(f"{what}: q_start must be [n_seqs + 1]")
+    own = (k.dtype,)
+    return dt, _ptr_here(k, own, what), _ptr_here(v, own, what), _ptr_here(q_start, _I32, what), n
+
+
+def mt_kv_store_f8(cache: mt_f8_cache, k_new, v_new, q_start, status=None, stream=None) -> None:
+    """Quantise rows into the 8-bit cache: the rows of sequence s,
+    q_start[s] .. q_start[s+1]-1, become its last positions. k_new, v_new
+    [n_tokens][n_kv_heads][head_dim] of float32, float16 or bfloat16."""
+    dt, k, v, qs, n = _f8_rows(cache, k_new, v_new, q_start, "mt_kv_store_f8")
+    _check(lib().mt_kv_store_f8(ctypes.byref(cache), dt, k, v, qs, n, _ptr(status),
+                                _stream(stream)), "mt_kv_store_f8")
+
+
+def mt_kv_load_f8(cache: mt_f8_cache, k_out, v_out, q_start, pos0=None, status=None,
+                  stream=None) -> None:
+    """Read rows of the 8-bit cache back into k_out, v_out: row j of sequence s
+    is position pos0[s] + j, or without pos0 its last positions."""
+    dt, k, v, qs, n = _f8_rows(cache, k_out, v_out, q_start, "mt_kv_load_f8")
+    if pos0 is not None and pos0.shape != (cache.n_seqs,):
+        raise ValueError("mt_kv_load_f8: pos0 must be [n_seqs]")
+    _check(lib().mt_kv_load_f8(ctypes.byref(cache), dt, k, v, qs, _ptr_here(pos0, _I32, "pos0"),
+                               n, _ptr(status), _stream(stream)), "mt_kv_load_f8")
+
+
+def f8_attn_args(cache: mt_f8_cache, q, out, *, scale, q_start=None, spans=None, kv_map=None,
+                 lse=None) -> mt_f8_attn_args:
+    """Arguments of attention over the 8-bit cache: q, out [n_tokens][n_heads]
+    [head_dim] of float32, float16 or bfloat16; lse float32 [n_tokens][n_heads];
+    spans int32 [n_tokens][2]; kv_map int32 [n_tokens][MT_KV_MAP_MAX_SPANS][2];
+    q_start int32 [n_seqs + 1] for prefill, absent for decode."""
+    n, hq, d = q.shape
+    if q.dtype not in _DTYPES or out.dtype != q.dtype:
+        raise ValueError("f8_attn_args: q and out must be float32, float16 or bfloat16, both alike")
+    if out.shape != q.shape or d != cache.head_dim:
+        raise ValueError("f8_attn_args: q and out must be [n_tokens][n_heads][head_dim]")
+    for t, shape, what in ((lse, (n, hq), "lse"), (spans, (n, 2), "spans"),
+                           (kv_map, (n, MT_KV_MAP_MAX_SPANS, 2), "kv_map"),
+                           (q_start, (cache.n_seqs + 1,), "q_start")):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"f8_attn_args: {what} must be {list(shape)}")
+    a = mt_f8_attn_args()
+    a.cache, a.dtype = cache, _DTYPES[q.dtype]
+    a.q, a.out = _ptr_here(q, (q.dtype,), "q"), _ptr_here(out, (q.dtype,), "out")
+    a.lse = _ptr_here(lse, _F32, "lse")
+    a.q_start, a.spans = _ptr_here(q_start, _I32, "q_start"), _ptr_here(spans, _I32, "spans")
+    a.kv_map = _ptr_here(kv_map, _I32, "kv_map")
+    a.n_tokens, a.n_heads, a.scale = n, hq, float(scale)
+    a._tensors = (cache, q, out, lse, q_start, spans, kv_map)
+    return a
+
+
+def mt_paged_attn_decode_f8_workspace_bytes(args: mt_f8_attn_args) -> int:
+    return int(lib().mt_paged_attn_decode_f8_workspace_bytes(ctypes.byref(args)))
+
+
+def mt_paged_attn_decode_f8(args: mt_f8_attn_args, workspace, stream=None) -> None:
+    """Decode attention over the 8-bit cache, one query per sequence."""
+    nbytes = workspace.numel() * workspace.element_size()
+    _check(lib().mt_paged_attn_decode_f8(ctypes.byref(args), _ptr(workspace), nbytes,
+                                         _stream(stream)), "mt_paged_attn_decode_f8")
 
 
 def _moves_array(moves):
