@@ -350,7 +350,7 @@ mt_status mt_paged_attn_decode_static(const mt_paged_attn_args *args, uint32_t *
  * the codes the block already holds are re-encoded; with powers of two that
  * only shifts exponents, so a value loses nothing unless it falls among the
  * subnormal codes (below 2^-6 of the scale). The reading calls take any
- * finite scales.
+ * finite scales that are not negative.
  */
 
 /* Element type of the dense arrays of these calls (new rows, rows read
@@ -444,6 +444,26 @@ size_t mt_paged_attn_decode_f8_workspace_bytes(const mt_f8_attn_args *args);
  * as one f16 for 16-bit outputs. */
 mt_status mt_paged_attn_decode_f8(const mt_f8_attn_args *args, void *workspace,
                                   size_t workspace_bytes, mt_stream stream);
+
+/* Workspace bytes of mt_paged_attn_prefill_f8 (0 on invalid args), with the
+ * conventions of mt_paged_attn_decode_f8_workspace_bytes. */
+size_t mt_paged_attn_prefill_f8_workspace_bytes(const mt_f8_attn_args *args);
+
+/* Multi-query (prefill, chunked prefill) attention over the 8-bit cache: the
+ * result that mt_paged_attn_prefill defines (causal, the n queries of a
+ * sequence being its last n positions; q_start, spans and kv_map as there), on
+ * the cache's values. head_dim 64 or 128, at most 8 query heads per KV head;
+ * others return MT_ERR_UNSUPPORTED. Out-of-range block ids and context
+ * lengths, query counts above the context length and query rows outside
+ * [0, n_tokens) are skipped and flagged in the workspace status word.
+ * Arithmetic: codes enter the tensor cores exactly (as f16), scales multiply
+ * in float32. 16-bit queries and their probabilities are one f16 each (bf16
+ * and f16 queries are exact but for elements 2^-26 below their row's largest);
+ * float32 queries and their probabilities a high and a low f16 part. A query
+ * that sees a position whose V holds a NaN gets NaN in all its dims; one that
+ * does not see it is not affected. */
+mt_status mt_paged_attn_prefill_f8(const mt_f8_attn_args *args, void *workspace,
+                                   size_t workspace_bytes, mt_stream stream);
 
 /* order_moves — "KV Cache Design — cells, format, sessions", section 2:
  * upward moves (dst > src) first, top-down (source descending), then

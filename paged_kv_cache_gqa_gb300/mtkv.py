@@ -126,6 +126,8 @@ def lib() -> ctypes.CDLL:
         "mt_kv_load_f8": (I, [ctypes.POINTER(mt_f8_cache), I, P, P, P, P, I, U32P, P]),
         "mt_paged_attn_decode_f8_workspace_bytes": (SZ, [ctypes.POINTER(mt_f8_attn_args)]),
         "mt_paged_attn_decode_f8": (I, [ctypes.POINTER(mt_f8_attn_args), P, SZ, P]),
+        "mt_paged_attn_prefill_f8_workspace_bytes": (SZ, [ctypes.POINTER(mt_f8_attn_args)]),
+        "mt_paged_attn_prefill_f8": (I, [ctypes.POINTER(mt_f8_attn_args), P, SZ, P]),
         "mt_order_moves": (I, [ctypes.POINTER(mt_move), I, ctypes.POINTER(I)]),
         "mt_check_moves": (I, [ctypes.POINTER(mt_move), I, I64, ctypes.POINTER(I)]),
         "mt_copy_cells": (I, [ctypes.POINTER(P), I, SZ, I64, ctypes.POINTER(mt_move), I, U32P,
@@ -441,6 +443,17 @@ def mt_paged_attn_decode_f8(args: mt_f8_attn_args, workspace, stream=None) -> No
     nbytes = workspace.numel() * workspace.element_size()
     _check(lib().mt_paged_attn_decode_f8(ctypes.byref(args), _ptr(workspace), nbytes,
                                          _stream(stream)), "mt_paged_attn_decode_f8")
+
+
+def mt_paged_attn_prefill_f8_workspace_bytes(args: mt_f8_attn_args) -> int:
+    return int(lib().mt_paged_attn_prefill_f8_workspace_bytes(ctypes.byref(args)))
+
+
+def mt_paged_attn_prefill_f8(args: mt_f8_attn_args, workspace, stream=None) -> None:
+    """Multi-query (prefill) attention over the 8-bit cache."""
+    nbytes = workspace.numel() * workspace.element_size()
+    _check(lib().mt_paged_attn_prefill_f8(ctypes.byref(args), _ptr(workspace), nbytes,
+                                          _stream(stream)), "mt_paged_attn_prefill_f8")
 
 
 def _moves_array(moves):

@@ -50,6 +50,8 @@ def test_bad_caches_are_refused(mt, bad, status):
     a = attn_of(mt, cache=c)
     assert L.mt_paged_attn_decode_f8(ctypes.byref(a), A, 1 << 40, None) == status
     assert L.mt_paged_attn_decode_f8_workspace_bytes(ctypes.byref(a)) == 0
+    assert L.mt_paged_attn_prefill_f8(ctypes.byref(a), A, 1 << 40, None) == status
+    assert L.mt_paged_attn_prefill_f8_workspace_bytes(ctypes.byref(a)) == 0
     assert mt.mt_last_error()
 
 
@@ -89,11 +91,31 @@ def test_bad_decode_arguments_are_refused(mt, bad, status):
     assert mt.mt_last_error()
 
 
+@pytest.mark.parametrize("bad,status", [
+    (dict(dtype=5), 1), (dict(n_heads=3), 1), (dict(n_heads=0), 1), (dict(n_heads=18), 2),
+    (dict(n_tokens=-3), 1), (dict(q_start=None), 1), (dict(spans=A, kv_map=A), 1),
+    (dict(q=None), 1), (dict(out=None), 1), (dict(q=A + 4), 1), (dict(out=A + 8), 1),
+    (dict(n_tokens=1 << 30), 2)])
+def test_bad_prefill_arguments_are_refused(mt, bad, status):
+    a = attn_of(mt, **{"n_tokens": 7, "q_start": A, **bad})
+    # (a size that only the device count limits is refused after the device query)
+    got = mt.lib().mt_paged_attn_prefill_f8(ctypes.byref(a), A, 1 << 40, None)
+    assert got == status or (bad.get("n_tokens") == 1 << 30 and got == mt.MT_ERR_CUDA)
+    assert mt.mt_last_error()
+
+
+def test_prefill_refuses_wide_heads(mt):
+    a = attn_of(mt, cache=cache_of(mt, head_dim=256), n_tokens=7, q_start=A)
+    assert mt.lib().mt_paged_attn_prefill_f8(ctypes.byref(a), A, 1 << 40, None) == \
+        mt.MT_ERR_UNSUPPORTED
+
+
 def test_null_arguments_are_refused(mt):
     L = mt.lib()
     assert L.mt_kv_store_f8(None, 0, A, A, A, 3, None, None) == mt.MT_ERR_INVALID_ARG
     assert L.mt_kv_load_f8(None, 0, A, A, A, None, 3, None, None) == mt.MT_ERR_INVALID_ARG
     assert L.mt_paged_attn_decode_f8(None, A, 1 << 40, None) == mt.MT_ERR_INVALID_ARG
+    assert L.mt_paged_attn_prefill_f8(None, A, 1 << 40, None) == mt.MT_ERR_INVALID_ARG
 
 
 def test_binding_refuses_tensors_of_other_places(mt):

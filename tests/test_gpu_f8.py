@@ -541,3 +541,241 @@ def test_calls_on_two_streams_at_once(mt):
     torch.cuda.synchronize()
     for _, _, out, lse, q, _ in sets:
         compare(out, lse, *oracle(w, q), "f32")
+
+
+# ----------------------------------------------------------------- prefill
+
+def run_prefill(w, cache, q, q_start, dt, want_status=0, **kw):
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+    kw = {k: dev(v) for k, v in kw.items()}
+    args = w.mt.f8_attn_args(cache, q, out, scale=w.d ** -0.5, lse=lse,
+                             q_start=dev(np.array(q_start, dtype=np.int32)), **kw)
+    need = w.mt.mt_paged_attn_prefill_f8_workspace_bytes(args)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    ws[:4] = 0
+    w.mt.mt_paged_attn_prefill_f8(args, ws)
+    assert w.mt.mt_check_device_status(ws) == want_status
+    return out, lse
+
+
+def starts(n):
+    return np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+
+
+@pytest.mark.parametrize("h,g,d,bs", [(2, 1, 64, 16), (1, 3, 64, 32), (2, 4, 128, 16),
+                                      (1, 8, 128, 32), (3, 7, 128, 16)])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("window", ["none", "spans", "runs"])
+def test_prefill_matches_the_oracle(mt, dt, h, g, d, bs, window):
+    # no queries, one, all positions, odd ends, more than one tile, holes; an
+    # empty sequence between others
+    ctx = [1, 60, 0, 300, 129, 200]
+    n = [1, 60, 0, 70, 1, 13]
+    w = World(mt, 51, ctx, h, d, bs, holes=0.2)
+    cache = w.upload()
+    qs = starts(n)
+    q, qd = w.q(int(qs[-1]), g, dt)
+    kw = {}
+    if window == "spans":
+        sp = np.stack([w.rng.integers(-20, 150, qs[-1]), w.rng.integers(0, 320, qs[-1])], 1)
+        kw = {"spans": sp.astype(np.int32)}
+    elif window == "runs":
+        kw = {"kv_map": runs_of(w.rng, int(qs[-1]), np.repeat(ctx, n))}
+    out, lse = run_prefill(w, cache, qd, qs, dt, **kw)
+    compare(out, lse, *oracle(w, q, q_start=qs, **kw), dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("h,g,d,n", [(1, 4, 128, 5), (2, 2, 64, 200), (8, 1, 128, 40)])
+def test_prefill_long_context_is_cut_into_pieces(mt, dt, h, g, d, n):
+    ctx = [2500, 40]
+    w = World(mt, 52, ctx, h, d, 16, holes=0.02)
+    cache = w.upload()
+    qs = starts([n, 3])
+    q, qd = w.q(int(qs[-1]), g, dt)
+    rows = sorted({0, 1, n // 2, n - 1, n, n + 2})
+    want, want_lse = oracle(w, q, q_start=qs, rows=rows)
+    out, lse = run_prefill(w, cache, qd, qs, dt)
+    compare(out[rows], lse[rows], want[rows], want_lse[rows], dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_many_units_a_cta(mt, dt, d):
+    # several units for every CTA, of unequal lengths: the hand-over from unit
+    # to unit, sampled rows of every sequence
+    rng = np.random.default_rng(53)
+    ctx = rng.integers(1, 700, 40)
+    n = np.minimum(rng.integers(1, 260, 40), ctx)
+    w = World(mt, 53, ctx, 8, d, 16)
+    cache = w.upload()
+    qs = starts(n)
+    q, qd = w.q(int(qs[-1]), 4, dt)
+    rows = sorted(set((qs[:-1]).tolist() + (qs[1:] - 1).tolist()
+                      + rng.integers(0, qs[-1], 30).tolist()))
+    want, want_lse = oracle(w, q, q_start=qs, rows=set(rows))
+    out, lse = run_prefill(w, cache, qd, qs, dt)
+    compare(out[rows], lse[rows], want[rows], want_lse[rows], dt)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+
+
+def test_prefill_window_far_from_the_start(mt):
+    # chunks before every query's window are not needed at all
+    ctx, n = [1500, 900], [20, 150]
+    w = World(mt, 54, ctx, 2, 128, 16)
+    for pool in w.pools:
+        for b in range(1500 // 16 - 30):
+            pool[w.table[0, b]] = 0x7f      # NaN where no query looks
+    cache = w.upload()
+    qs = starts(n)
+    q, qd = w.q(int(qs[-1]), 2, "bf16")
+    pos = np.concatenate([np.arange(1480, 1500), np.arange(750, 900)])
+    sp = np.stack([np.maximum(pos - 400, 0), pos + 1], 1).astype(np.int32)
+    out, lse = run_prefill(w, cache, qd, qs, "bf16", spans=sp)
+    compare(out, lse, *oracle(w, q, q_start=qs, spans=sp), "bf16")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+def test_prefill_nan_reaches_only_those_who_see_it(mt, dt):
+    ctx = [200]
+    w = World(mt, 55, ctx, 2, 64, 16)
+    clean = [p.copy() for p in w.pools]
+    w.pools[0][w.table[0, 150 // 16], 150 % 16, 0, 5] = 0x7f   # K of position 150, head 0
+    w.pools[1][w.table[0, 170 // 16], 170 % 16, 1, 9] = 0xff   # V of position 170, head 1
+    # slots past the context hold NaN too
+    for p in w.pools:
+        p[w.table[0, 199 // 16], 8:] = 0x7f
+    cache = w.upload()
+    q, qd = w.q(100, 2, dt)
+    out, lse = run_prefill(w, cache, qd, [0, 100], dt)
+    w.pools = clean
+    want, want_lse = oracle(w, q, q_start=[0, 100])
+    pos = np.arange(100, 200)
+    hit = np.stack([pos >= 150, pos >= 150, pos >= 170, pos >= 170], 1)
+    o, ls = out.double().cpu().numpy(), lse.cpu().numpy()
+    assert np.isnan(o[hit]).all() and np.isnan(ls[hit]).all()
+    tol = 1e-4 + STEP[dt] * np.abs(want[~hit]) + (0 if dt == "f32" else 2.0 ** -11 * 6)
+    assert (np.abs(o[~hit] - want[~hit]) <= tol).all()
+    assert np.abs(ls[~hit] - want_lse[~hit]).max() <= 1e-4
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+def test_prefill_extreme_magnitudes(mt, dt):
+    # V scales that differ by 2^30 between blocks, rising along the sequence,
+    # and one block of zeros; tiny and huge K scales against the queries
+    h, g, d, bs = 1, 4, 128, 16
+    w = World(mt, 56, [400], h, d, bs)
+    w.scales[0] *= np.float32(2.0 ** 12)
+    for b in range(25):
+        w.scales[1][w.table[0, b]] *= np.float32(2.0 ** (b - 12))
+    w.scales[1][w.table[0, 4]] = 0.0
+    cache = w.upload()
+    q, _ = w.q(33, g, "f32")
+    q = rounded(q * 2.0 ** -12, dt)
+    out, lse = run_prefill(w, cache, dev(q).to(DT[dt]), [0, 33], dt)
+    want, want_lse = oracle(w, q, q_start=[0, 33])
+    # errors scale with the largest values around (2^12 times N(0, 1))
+    tol = 2.0 ** 12 * (1e-4 + (0 if dt == "f32" else 2.0 ** -11 * 6)) + STEP[dt] * np.abs(want)
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+    assert np.abs(lse.cpu().numpy() - want_lse).max() <= 1e-4
+
+
+def test_prefill_negative_softmax_scale(mt):
+    w = World(mt, 57, [150], 1, 64, 16)
+    cache = w.upload()
+    q, qd = w.q(20, 2, "f32")
+    out, lse = torch.empty_like(qd), torch.empty(20, 2, device="cuda")
+    args = mt.f8_attn_args(cache, qd, out, scale=-0.125, lse=lse, q_start=dev(starts([20])))
+    ws = torch.zeros(mt.mt_paged_attn_prefill_f8_workspace_bytes(args), dtype=torch.uint8,
+                     device="cuda")
+    mt.mt_paged_attn_prefill_f8(args, ws)
+    want = f8.attention(q, *w.pools, *w.scales, w.table, w.ctx, 16, -0.125, q_start=[0, 20])
+    compare(out, lse, *want, "f32")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_prefill_leaves_other_rows_and_flags_bad_input(mt, dt):
+    w = World(mt, 58, [40, 30, 50], 2, 64, 16)
+    w.table[2, 1] = w.n_phys + 1
+    cache = w.upload()
+    # rows behind the last sequence are not written
+    q, qd = w.q(30, 2, dt)
+    out, lse = run_prefill(w, cache, qd, [3, 13, 13, 23], dt, want_status=mt.MT_ERR_DEVICE_CHECK)
+    rest = list(range(3)) + list(range(23, 30))
+    assert out[rest].isnan().all() and lse[rest].isnan().all()
+    w.table[2, 1] = -1
+    want, want_lse = oracle(w, q, q_start=[3, 13, 13, 23], rows=set(range(3, 23)))
+    compare(out[3:23], lse[3:23], want[3:23], want_lse[3:23], dt)
+    # more queries than positions: those without one see nothing
+    out, lse = run_prefill(w, w.upload(), qd, [0, 0, 30, 30], dt)
+    w.ctx[1] = 20
+    out2, lse2 = run_prefill(w, w.upload(), qd, [0, 0, 30, 30], dt,
+                             want_status=mt.MT_ERR_DEVICE_CHECK)
+    assert (out2[:10] == 0).all() and lse2[:10].isneginf().all()
+    want, want_lse = f8.attention(q[10:], *w.pools, *w.scales, w.table[1:2], w.ctx[1:2], 16,
+                                  w.d ** -0.5, q_start=[0, 20])
+    compare(out2[10:], lse2[10:], want, want_lse, dt)
+    # rows outside the array, a falling q_start
+    for bad in ([0, 0, 31, 31], [-2, 5, 5, 5], [9, 4, 4, 4]):
+        out, _ = run_prefill(w, cache, qd, bad, dt, want_status=mt.MT_ERR_DEVICE_CHECK)
+        assert out.isnan().all()
+
+
+def test_prefill_chunks_equal_decode_and_one_prefill(mt):
+    # a prompt stored and attended in chunks, then a decode step: the same rows
+    # as one prefill over the whole, within the rounding of each
+    h, g, d, bs, dt = 2, 4, 128, 16, "bf16"
+    w = World(mt, 59, [300], h, d, bs)
+    w.upload()
+    table, ctx = dev(w.table), torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = mt.f8_cache(*w.dp, *w.ds, table, ctx)
+    done = 0
+    for n in (128, 100, 71, 1):
+        done += n
+        ctx.fill_(done)
+        qs = dev(starts([n]))
+        new = [rounded(w.rng.normal(size=(n, h, d)), dt) for _ in range(2)]
+        mt.mt_kv_store_f8(cache, *[dev(x).bfloat16() for x in new], qs)
+        w.ctx[0] = done
+        for x, pool, sc in zip(new, w.pools, w.scales):
+            f8.store(pool, sc, x, w.table, w.ctx, [0, n], bs)
+        q, qd = w.q(n, g, dt)
+        want = oracle(w, q, q_start=[0, n])
+        compare(*run_prefill(w, cache, qd, [0, n], dt), *want, dt)
+        if n == 1:
+            compare(*run_decode(w, cache, qd, dt), *want, dt)
+    check_cache(w)
+
+
+def test_prefill_captured_into_a_graph_and_on_two_streams(mt):
+    w = World(mt, 60, [900, 200], 2, 128, 16)
+    cache = w.upload()
+    qs = starts([40, 100])
+    sets = []
+    for _ in range(2):
+        q, qd = w.q(140, 4, "f16")
+        out, lse = torch.empty_like(qd), torch.empty(140, 8, device="cuda")
+        args = mt.f8_attn_args(cache, qd, out, scale=w.d ** -0.5, lse=lse, q_start=dev(qs))
+        ws = torch.zeros(mt.mt_paged_attn_prefill_f8_workspace_bytes(args), dtype=torch.uint8,
+                         device="cuda")
+        sets.append((args, ws, out, lse, q, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for args, ws, _, _, _, st in sets:
+            mt.mt_paged_attn_prefill_f8(args, ws, stream=st)
+    torch.cuda.synchronize()
+    for _, _, out, lse, q, _ in sets:
+        compare(out, lse, *oracle(w, q, q_start=qs), "f16")
+    args, ws, out, lse, q, _ = sets[0]
+    first = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mt.mt_paged_attn_prefill_f8(args, ws)
+        mt.mt_paged_attn_prefill_f8(sets[1][0], ws)   # the same workspace, in order
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+        compare(sets[1][2], sets[1][3], *oracle(w, sets[1][4], q_start=qs), "f16")
