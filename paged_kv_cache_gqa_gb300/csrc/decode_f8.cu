@@ -128,6 +128,16 @@ __device__ __forceinline__ int steps_of(int lo, int hi) {
   return hi > lo ? (hi - 1) / kStep - lo / kStep + 1 : 0;
 }
 
+__device__ __forceinline__ long long warp_incl(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(kAll, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
 // Steps of all sequences before s, and of all sequences: the whole warp takes part.
 __device__ __forceinline__ void count_steps(const DecodeParams &p, int s, long long &before,
                                             long long &total) {
@@ -152,6 +162,13 @@ __device__ __forceinline__ int ctas_used(const DecodeParams &p, long long total)
   return (int)max(1LL, min((long long)p.n_ctas, total / kMinSteps));
 }
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool ok) {
   const int n = ok ? BYTES : 0;  // 0: nothing is read, the destination is zero-filled
@@ -224,13 +241,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   long long r0 = 0, r1 = 0;
   int s = 0, hg = 0;       // where it starts
   long long skip = 0;      // steps of (s, hg) before the range
+  int w_lo = 0, w_hi = 0;  // sequence `lane`'s window (B <= 32)
   if (p.whole) {
     s = blockIdx.x / p.n_hg;
     hg = blockIdx.x % p.n_hg;
     r1 = INT_MAX;
   } else {
-    long long before, total;
-    count_steps(p, 0, before, total);
+    long long total = 0, before = 0, incl;
+    int k = 0;
+    if (p.B <= 32) {
+      // every window is loaded once, and kept: lane t has sequence t's
+      if (lane < p.B) window(p, lane, w_lo, w_hi);
+      k = steps_of(w_lo, w_hi);
+      incl = warp_incl(k);
+      total = __shfl_sync(kAll, incl, 31);
+    } else {
+      count_steps(p, 0, before, total);
+    }
     total *= p.n_hg;
     const int n = ctas_used(p, total);
     if ((int)blockIdx.x >= n) return;
@@ -240,31 +267,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     // the sequence that holds unit r0: prefix sums of 32 sequences at a time
     long long run = 0;
     for (int b0 = 0;; b0 += 32) {
-      int k = 0;
-      if (b0 + lane < p.B) {
-        int lo, hi;
-        window(p, b0 + lane, lo, hi);
-        k = steps_of(lo, hi);
+      if (p.B > 32) {
+        k = 0;
+        if (b0 + lane < p.B) {
+          int lo, hi;
+          window(p, b0 + lane, lo, hi);
+          k = steps_of(lo, hi);
+        }
+        incl = warp_incl(k);
       }
-      long long incl = (long long)k * p.n_hg;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const uint32_t past = __ballot_sync(kAll, run + incl > r0);
+      const uint32_t past = __ballot_sync(kAll, run + incl * p.n_hg > r0);
       if (past) {
         const int l = __ffs(past) - 1;
         s = b0 + l;
         const int ks = __shfl_sync(kAll, k, l);
-        const long long off = r0 - (run + __shfl_sync(kAll, incl, l) - (long long)ks * p.n_hg);
+        const long long off = r0 - run - (__shfl_sync(kAll, incl, l) - ks) * p.n_hg;
         hg = (int)(off / ks);
         skip = off % ks;
         break;
       }
-      run += __shfl_sync(kAll, incl, 31);
+      run += __shfl_sync(kAll, incl, 31) * p.n_hg;
     }
   }
+  auto window_of = [&](int t, int &lo, int &hi) {
+    if (!p.whole && p.B <= 32) {
+      lo = __shfl_sync(kAll, w_lo, t);
+      hi = __shfl_sync(kAll, w_hi, t);
+    } else {
+      window(p, t, lo, hi);
+    }
+  };
 
   long long left = r1 - r0;
   const int head_l = warp % p.hc, slice = warp / p.hc;  // within the head group
@@ -272,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   while (left > 0 && s < p.B) {
     // ---- a segment: steps [a, b) of (s, hg)
     int lo, hi;
-    window(p, s, lo, hi);
+    window_of(s, lo, hi);
     const int n_all = steps_of(lo, hi);
     const int a = (int)skip;
     const int b = (int)min((long long)n_all, skip + left);
@@ -326,48 +358,71 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
       auto scale_of = [&](const float *sc, int id) -> float {
         return id >= 0 ? __ldg(sc + (size_t)id * p.H + kvh) : 0.f;
       };
-      int id_n = fetch_id(lane);
-      check_id(id_n);
-      put(lane, id_n, scale_of(p.k_scales, id_n), scale_of(p.v_scales, id_n));
-      id_n = fetch_id(32 + lane);
+      int id_0 = fetch_id(lane);
+      check_id(id_0);
+      put(lane, id_0, 0.f, 0.f);
+      int id_n = fetch_id(32 + lane);
       float ks_n = 0.f, vs_n = 0.f;
       __syncwarp();
 
-      // ---- the copies of step k into its queue slot
-      const size_t row = (size_t)p.H * D;
+      // ---- the copies of step k into its queue slot: a lane's bytes of 8 rows
+      // apart (K) or of rows 2c, 2c + 1, 8 + 2c, 9 + 2c (V), at fixed offsets from
+      // the step's first cell
+      const uint32_t row = (uint32_t)p.H * D;
+      const uint8_t *k_l = p.k_pool + (size_t)kvh * D + (size_t)g * row + 16 * c;
+      const uint8_t *v_l = p.v_pool + (size_t)kvh * D + (size_t)(2 * c) * row + C::VB * g;
+      uint32_t dst = ring_a + lane * 16;  // of the step to be issued
+      int i_slot = 0;
       auto issue = [&](int k) {
         if (k < n_mine) {
           const Meta &mt = meta[k & (kMeta - 1)];
           const uint32_t mask = mt.mask;
-          const uint32_t dst = ring_a + (uint32_t)(k % ST) * C::STAGE;
           const int half = p.bs_shift == 5 ? ((step0 + k * p.slices) & 1) * kStep : 0;
-          const size_t base = (((size_t)max(mt.phys, 0) << p.bs_shift) + half) * row + (size_t)kvh * D;
+          // (a hole's step copies nothing, from a valid address)
+          const size_t base = (((size_t)max(mt.phys, 0) << p.bs_shift) + half) * row;
+          const uint32_t vdst = dst + kStep * D - lane * (16 - C::VB);
+          const uint8_t *ks = k_l + base, *vs = v_l + base;
+          if (mask == 0xffffu) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int r = 8 * t + g;
-            const bool ok = (mask >> r) & 1u;
-            const uint8_t *src = p.k_pool + base + (size_t)r * row + 16 * c;
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int j = 0; j < C::KP; ++j)
-              copy_async<16>(dst + (t * C::KP + j) * 512 + lane * 16, ok ? src + 64 * j : p.k_pool,
-                             ok);
+              for (int j = 0; j < C::KP; ++j)
+                copy_async<16>(dst + (t * C::KP + j) * 512, ks + t * (8 * row) + 64 * j);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int j = 0; j < C::VP; ++j)
+                copy_async<C::VB>(vdst + (t * C::VP + j) * (32 * C::VB),
+                                  vs + ((t & 1) + 8 * (t >> 1)) * row + 128 * j);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < C::KP; ++j)
+                copy_async<16>(dst + (t * C::KP + j) * 512, ks + t * (8 * row) + 64 * j,
+                               (mask >> (8 * t + g)) & 1u);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int j = 0; j < C::VP; ++j)
+                copy_async<C::VB>(vdst + (t * C::VP + j) * (32 * C::VB),
+                                  vs + ((t & 1) + 8 * (t >> 1)) * row + 128 * j,
+                                  (mask >> (2 * c + (t & 1) + 8 * (t >> 1))) & 1u);
           }
-          const uint32_t vdst = dst + kStep * D;
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int r = 2 * c + (t & 1) + 8 * (t >> 1);
-            const bool ok = (mask >> r) & 1u;
-            const uint8_t *src = p.v_pool + base + (size_t)r * row + C::VB * g;
-#pragma unroll
-            for (int j = 0; j < C::VP; ++j)
-              copy_async<C::VB>(vdst + (t * C::VP + j) * (32 * C::VB) + lane * C::VB,
-                                ok ? src + 128 * j : p.v_pool, ok);
+          dst += C::STAGE;
+          if (++i_slot == ST) {
+            i_slot = 0;
+            dst -= ST * C::STAGE;
           }
         }
         copy_commit();
       };
 #pragma unroll
       for (int k = 0; k < ST - 1; ++k) issue(k);
+      // scales of the first batch, once its copies are under way
+      meta[lane].ks = scale_of(p.k_scales, id_0);
+      meta[lane].vs = scale_of(p.v_scales, id_0);
+      __syncwarp();
 
       // ---- the group's queries as A fragments: q / 2^e in high and low f16
       // parts, 2^e bringing the row's largest value to [2^11, 2^12)
@@ -401,7 +456,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         }
       }
 
-      for (int k = 0; k < n_mine; ++k) {
+      uint32_t st = ring_a + lane * 16;  // of the step to be used
+      int u_slot = 0;
+      float v_inv = 0.f;                 // 1 / v_ref
+#pragma unroll 1
+      for (int k = 0; k < n_mine; ++k, st += C::STAGE) {
+        if (u_slot == ST) {
+          u_slot = 0;
+          st -= ST * C::STAGE;
+        }
+        ++u_slot;
         const int ki = k + ST - 1;  // the step whose copies start now
         if ((ki & 31) == 16) {
           check_id(id_n);
@@ -419,16 +483,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         copy_wait<ST - 1>();
         const Meta mt = meta[k & (kMeta - 1)];
         if (mt.mask == 0u) continue;
-        const uint32_t st = ring_a + (uint32_t)(k % ST) * C::STAGE;
 
         // ---- scores
+        uint4 kw[2][C::KP];
+#pragma unroll
+        for (int j = 0; j < C::KP; ++j)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kw[t][j] = lds16(st + (t * C::KP + j) * 512);
         float sc[2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < C::KP; ++j) {
-            const uint4 w = lds16(st + (t * C::KP + j) * 512 + lane * 16);
+            const uint4 w = kw[t][j];
             uint32_t b0, b1;
             f8::code4_to_h2(w.x, b0, b1);
             mma_f16(s0, qa[4 * j], b0, b1);
@@ -442,6 +510,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[t][i] = s0[i] + s1[i];
         }
+        // V's first piece, on its way while the softmax runs
+        const uint32_t vt = st + kStep * D - lane * (16 - C::VB);
+        uint32_t w[4][C::VB / 4];
+        auto load_v = [&](int j) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t at = vt + (t * C::VP + j) * (32 * C::VB);
+            if constexpr (C::VB == 16) {
+              const uint4 u = lds16(at);
+              w[t][0] = u.x;
+              w[t][1] = u.y;
+              w[t][2] = u.z;
+              w[t][3] = u.w;
+            } else {
+              const uint2 u = lds8(at);
+              w[t][0] = u.x;
+              w[t][1] = u.y;
+            }
+          }
+        };
+        load_v(0);
         // head g's scores at positions 2c, 2c + 1, 8 + 2c, 9 + 2c
         const float f = qfac * mt.ks;
         float x[4] = {(sc[0][0] + sc[0][2]) * f, (sc[0][1] + sc[0][3]) * f,
@@ -467,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
           const float v_new = fmaxf(v_ref, mt.vs);
           al *= v_new > 0.f ? v_ref / v_new : 1.f;
           v_ref = v_new;
+          v_inv = 1.f / fmaxf(v_new, 1.17549435e-38f);
           const float a0 = __shfl_sync(kAll, al, 8 * c), a1 = __shfl_sync(kAll, al, 8 * c + 4);
 #pragma unroll
           for (int m = 0; m < C::MT; ++m) {
@@ -478,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         }
         // ---- probabilities
         const float mr = m_run == -INFINITY ? 0.f : m_run;
-        const float wv = v_ref > 0.f ? 128.f * (mt.vs / v_ref) : 0.f;
+        const float wv = mt.vs * v_inv * 128.f;
         float pr[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -490,25 +580,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         split_h2(pr[0], pr[1], ph[0], pl[0]);
         split_h2(pr[2], pr[3], ph[1], pl[1]);
         // ---- O^T += V^T P^T
-        const uint32_t vt = st + kStep * D;
 #pragma unroll
         for (int j = 0; j < C::VP; ++j) {
-          uint32_t w[4][C::VB / 4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t at = vt + (t * C::VP + j) * (32 * C::VB) + lane * C::VB;
-            if constexpr (C::VB == 16) {
-              const uint4 u = lds16(at);
-              w[t][0] = u.x;
-              w[t][1] = u.y;
-              w[t][2] = u.z;
-              w[t][3] = u.w;
-            } else {
-              const uint2 u = lds8(at);
-              w[t][0] = u.x;
-              w[t][1] = u.y;
-            }
-          }
+          if (j > 0) load_v(j);
 #pragma unroll
           for (int i = 0; i < C::VB / 4; ++i) {
             uint32_t a0[4], a1[4];
@@ -621,27 +695,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
       do {
         ++s;
         if (s >= p.B) break;
-        window(p, s, lo, hi);
+        window_of(s, lo, hi);
       } while (hi <= lo);
     }
   }
 }
 
-// Merge the partial results of split (sequence, head group)s, a CTA per
-// (sequence, query head): warps take the pieces in turn, then merge through
-// shared memory. Sequences that see nothing get 0 and -infinity here; those
-// that one CTA finished are left alone.
-constexpr int kMergeWarps = 4;
+// Merge the partial results of split (sequence, head group)s: MW warps for each
+// (sequence, query head) take its pieces in turn, then merge through shared
+// memory. One warp when there are rows enough for every SM and few pieces a row,
+// else all eight of a CTA. Sequences that see nothing get 0 and -infinity here;
+// those that one CTA finished are left alone.
+constexpr int kMergeWarps = 8;
 
-template <int D, int DT>
+template <int D, int DT, int MW>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     merge_f8_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int DV = D / 32;
-  __shared__ float o_s[kMergeWarps][D];
-  __shared__ float2 ml_s[kMergeWarps];
+  __shared__ float o_s[MW > 1 ? MW : 1][MW > 1 ? D : 1];
+  __shared__ float2 ml_s[MW];
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int s = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+  const int wi = warp % MW;  // of this row's warps
+  const int row = blockIdx.x * (kMergeWarps / MW) + warp / MW;
+  const bool live = row < p.B * p.Hq;
+  const int s = live ? row / p.Hq : 0, h = live ? row % p.Hq : 0;
   const int kvh = h / p.G, hg = kvh / p.hc;
   // lengths and windows are inputs: read before the decode kernel has ended
   long long before, total;
@@ -661,14 +739,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   // every CTA waits, also one with nothing to merge: this grid must not
   // complete before the decode has, or the stream's next kernel could start
   pdl_wait();
-  if (c0 == c1) return;
+  if (!live || c0 == c1) return;  // (with MW > 1 the whole CTA is this row's)
   const int hin = (kvh - hg * p.hc) * p.G + h % p.G, per = p.hc * p.G;
   float M = -INFINITY, L = 0.f, acc[DV];
 #pragma unroll
   for (int e = 0; e < DV; ++e) acc[e] = 0.f;
   const size_t slot0 = (size_t)s * p.n_hg + hg;
 #pragma unroll 4
-  for (int i = c0 + warp; i <= c1; i += kMergeWarps) {
+  for (int i = c0 + wi; i <= c1; i += MW) {
     const size_t rec = (slot0 + i) * per + hin;
     const float2 ml = __ldcg(p.part_ml + rec);
     float v[DV];
@@ -680,37 +758,45 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     }
     if (ml.x == -INFINITY && ml.y == 0.f) continue;  // a piece that saw nothing
     const float m_new = fmaxf(M, ml.x);
-    const float f0 = M == -INFINITY ? 0.f : ex2(M - m_new), f1 = ex2(ml.x - m_new);
+    const float f0 = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : ex2(M - m_new);
+    const float f1 = ml.x == -INFINITY ? 1.f : ex2(ml.x - m_new);  // (its sum is a NaN)
     M = m_new;
     L = L * f0 + ml.y * f1;
 #pragma unroll
     for (int e = 0; e < DV; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
   }
-  if (lane == 0) ml_s[warp] = make_float2(M, L);
+  if constexpr (MW > 1) {
+    if (lane == 0) ml_s[wi] = make_float2(M, L);
 #pragma unroll
-  for (int e = 0; e < DV; ++e) o_s[warp][lane * DV + e] = acc[e];
-  __syncthreads();
-  M = -INFINITY;
+    for (int e = 0; e < DV; ++e) o_s[wi][lane * DV + e] = acc[e];
+    __syncthreads();
+    if (wi > 0) return;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, ml_s[w].x);
-  L = 0.f;
-  float f[kMergeWarps];
+    for (int w = 1; w < MW; ++w) M = fmaxf(M, ml_s[w].x);
+    L = 0.f;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    f[w] = ml_s[w].x == -INFINITY ? (ml_s[w].y == 0.f ? 0.f : 1.f) : ex2(ml_s[w].x - M);
-    L += ml_s[w].y * f[w];
+    for (int e = 0; e < DV; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < MW; ++w) {
+      const float2 ml = ml_s[w];
+      const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
+      L += ml.y * f;
+#pragma unroll
+      for (int e = 0; e < DV; ++e) acc[e] += o_s[w][lane * DV + e] * f;
+    }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const size_t orow = ((size_t)s * p.Hq + h) * D;
-  for (int d = threadIdx.x * 4; d < D; d += 128 * kMergeWarps) {
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
+  const size_t o = ((size_t)s * p.Hq + h) * D + lane * DV;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] += o_s[w][d + e] * f[w];
-    f8::store4<DT>(p.out, orow + d, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  for (int e = 0; e < DV; e += 2) {
+    if constexpr (DT == MT_F32)
+      *reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.out) + o + e) =
+          make_float2(acc[e] * inv, acc[e + 1] * inv);
+    else
+      reinterpret_cast<uint32_t *>(p.out)[(o + e) / 2] =
+          f8::pack2<DT>(acc[e] * inv, acc[e + 1] * inv);
   }
-  if (p.lse && threadIdx.x == 0)
+  if (p.lse && lane == 0)
     p.lse[(size_t)s * p.Hq + h] =
         L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
@@ -793,8 +879,12 @@ mt_status launch(const Plan &pl, cudaStream_t s) {
   st = cuda_check(launch_pdl(kern, dim3((unsigned)pl.ctas), dim3(kThreads), smem, s, pl.p),
                   "f8 decode launch");
   if (st != MT_OK || pl.p.whole) return st;
-  return cuda_check(launch_pdl(merge_f8_kernel<D, DT>, dim3((unsigned)(pl.p.B * pl.p.Hq)),
-                               dim3(32 * kMergeWarps), 0, s, pl.p),
+  // pieces a row: the grid's CTAs over the rows' head groups, at the least
+  const long long rows = (long long)pl.p.B * pl.p.Hq;
+  const bool few = pl.ctas <= 8LL * pl.p.B * pl.p.n_hg;
+  auto merge = few ? merge_f8_kernel<D, DT, 1> : merge_f8_kernel<D, DT, kMergeWarps>;
+  const long long grid = few ? (rows + kMergeWarps - 1) / kMergeWarps : rows;
+  return cuda_check(launch_pdl(merge, dim3((unsigned)grid), dim3(32 * kMergeWarps), 0, s, pl.p),
                     "f8 decode merge launch");
 }
 
