@@ -14,11 +14,13 @@
 //    from the context lengths. A CTA's warps take the KV heads of the same
 //    steps (and, with few KV heads, interleaved steps), so the lines they
 //    read together form whole blocks of the pool.
-//  * A warp computes 16 positions of one KV head with mma.sync.m16n8k16 and
-//    reads every code from global memory once, by 16-byte asynchronous copies
-//    into a shared-memory queue that is private to the lane: a lane copies
-//    exactly the bytes it uses, so neither barriers nor bank conflicts nor
-//    shuffles come between memory and the matrix instructions.
+//  * The cells of a step, all heads, arrive by one bulk copy each of K and V
+//    (tensor copies with the 128-byte swizzle where rows are whole 128-byte
+//    lines, so that the lanes' reads spread over the banks), into a ring that the
+//    first warp of the heads' warps fills. (Copies by every lane of the bytes it
+//    uses, a head's 128 bytes of every row apart, reached 4.3 TB/s with or
+//    without the arithmetic: the accesses, not the work, were the bound.)
+//  * A warp computes 16 positions of one KV head with mma.sync.m16n8k16:
 //      S = Q K^T: rows 0..7 of A are the high f16 parts of the group's
 //      queries, rows 8..15 the low parts. The k index of the product may run
 //      over the dims in any order, so k step j of lane group c stands for
@@ -43,6 +45,7 @@
 #include "f8.cuh"
 #include "f8.h"
 #include "mma.cuh"
+#include "tmap.h"
 
 namespace mtkv {
 namespace {
@@ -52,11 +55,21 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;           // positions of a step
 constexpr int kMaxG = 8;            // query heads per KV head
-constexpr int kMeta = 64;           // step records per warp: two batches of 32
+constexpr int kBatch = 8;           // step records read at a time
+constexpr int kMeta = 2 * kBatch;   // step records per warp
+constexpr int kMaxStages = 8;
+constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMinSteps = 8;        // steps of a CTA's range, at least
 constexpr int kHdrBytes = 256;      // status word and padding at the workspace's start
 
+// How a step's cells are copied: all rows as one tensor copy (rows of whole
+// 128-byte lines, staged with an odd number of lines), all rows as one bulk copy
+// (other rows, at their own pitch), or row by row (a head group of several: its
+// part of each row, 16 bytes between them).
+enum : int { kTensor = 0, kWhole = 1, kRowwise = 2 };
+
 struct DecodeParams {
+  CUtensorMap map_k, map_v;  // kTensor
   const uint8_t *k_pool, *v_pool;
   const float *k_scales, *v_scales;
   const int32_t *table, *ctx, *spans, *kv_map;
@@ -69,6 +82,9 @@ struct DecodeParams {
   int B, Hq, H, G, max_blocks, bs_shift;
   int hc, n_hg;      // KV heads of a head group, head groups
   int slices;        // warps that share a KV head's steps
+  int copy;          // kTensor, kWhole or kRowwise
+  int pitch;         // staged bytes of a row
+  int stages, stage_bytes;
   int whole;         // 1: CTA i takes all steps of (sequence, head group) i
   int n_ctas;
   long long n_phys;
@@ -82,10 +98,11 @@ struct Cfg {
   static constexpr int VP = D / 8 / VB;            // V pieces per position of a lane
   static constexpr int KS = D / 16;                // k steps of Q K^T
   static constexpr int MT = D / 16;                // dim tiles of O
-  static constexpr int STAGE = 2 * kStep * D;      // bytes of a step's K and V
-  static constexpr int STAGES = D == 64 ? 6 : 3;
   static constexpr int CTAS = D == 256 ? 1 : 2;    // per SM
-  static constexpr int SMEM = kWarps * (STAGES * STAGE + kMeta * 16);
+  // shared memory of a CTA: the ring, then the step records
+  // (two CTAs of 111 KB, their barriers and the system's 1 KB each fill the SM)
+  static constexpr int SMEM = CTAS == 1 ? 224 * 1024 : 111 * 1024;
+  static constexpr int META = kWarps * kMeta * 16;
 };
 
 struct Meta {
@@ -162,29 +179,22 @@ __device__ __forceinline__ int ctas_used(const DecodeParams &p, long long total)
   return (int)max(1LL, min((long long)p.n_ctas, total / kMinSteps));
 }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+// 16 rows of all heads (kTensor): box (64, lines, 16) of [cell][line][64 x 16 bit].
+__device__ __forceinline__ void copy_tensor(uint32_t dst, const CUtensorMap *map, int cell,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(cell), "r"(smem_u32(bar))
+      : "memory");
 }
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool ok) {
-  const int n = ok ? BYTES : 0;  // 0: nothing is read, the destination is zero-filled
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -227,14 +237,49 @@ template <int D, int DT>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     decode_f8_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<D>;
-  constexpr int ST = C::STAGES;
   constexpr bool PLO = DT == MT_F32;  // low parts of the probabilities too
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kWarps * kMaxStages], empty[kWarps * kMaxStages];
+  __shared__ int abort_s;
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  uint8_t *ring = smem + warp * (ST * C::STAGE);
-  Meta *meta = reinterpret_cast<Meta *>(smem + kWarps * ST * C::STAGE) + warp * kMeta;
-  const uint32_t ring_a = smem_u32(ring);
+  const int head_l = warp % p.hc, slice = warp / p.hc;  // within the head group
+  const bool leader = head_l == 0 && slice < p.slices;  // fills its slice's ring
+  const int ST = p.stages;
+  const uint32_t ring_a = smem_u32(smem) + (uint32_t)(slice * ST * p.stage_bytes);
+  uint64_t *full_r = full + slice * ST, *empty_r = empty + slice * ST;
+  Meta *meta = reinterpret_cast<Meta *>(smem + C::SMEM - 1024 - C::META) + warp * kMeta;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.slices * ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], p.hc);
+    }
+    abort_s = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  // this lane's bytes of a staged step: K rows 8 t + g, dims 64 j + 16 c ..; V rows
+  // 2c, 2c + 1, 8 + 2c, 9 + 2c, dims 128 j + VB g ..
+  auto staged = [&](int row, int byte) -> uint32_t {
+    if (p.copy != kTensor) return (uint32_t)(row * p.pitch + byte);
+    const int line = row * (p.pitch >> 7) + (byte >> 7);
+    return (uint32_t)(line * 128 + ((((byte >> 4) & 7) ^ (line & 7)) << 4) + (byte & 15));
+  };
+  uint32_t k_at[2][C::KP], v_at[4][C::VP];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int j = 0; j < C::KP; ++j) k_at[t][j] = staged(8 * t + g, head_l * D + 64 * j + 16 * c);
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int j = 0; j < C::VP; ++j)
+      v_at[t][j] = p.stage_bytes / 2 +
+                   staged(2 * c + (t & 1) + 8 * (t >> 1), head_l * D + 128 * j + C::VB * g);
+  bool fine = true;            // false once a bounded wait ran out: no more waits or copies
+  int u_slot = 0, u_par = 0;   // ring place of the next step to use, and its parity
+  int i_slot = 0, i_par = 1;   // of the next step to fill (parity of its emptying)
   pdl_enter();
 
   // ---- this CTA's range of the stream (sequence, head group, step)
@@ -299,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   };
 
   long long left = r1 - r0;
-  const int head_l = warp % p.hc, slice = warp / p.hc;  // within the head group
   int slot_cta = blockIdx.x;
   while (left > 0 && s < p.B) {
     // ---- a segment: steps [a, b) of (s, hg)
@@ -310,8 +354,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     const int b = (int)min((long long)n_all, skip + left);
     const int kvh = hg * p.hc + head_l;
     const bool mine = slice < p.slices && kvh < p.H;
-    const int n_mine = mine && a + slice < b ? (b - a - slice + p.slices - 1) / p.slices : 0;
+    // steps of this warp's slice, and its own (none without a head)
+    const int n_slice = a + slice < b ? (b - a - slice + p.slices - 1) / p.slices : 0;
+    const int n_mine = mine ? n_slice : 0;
     const int step0 = lo / kStep + a + slice;
+    // a step's data are in place / no longer needed by this warp; every warp of
+    // the slice, with a head or without, takes part in every step, so none can be
+    // a ring's round ahead of the others
+    auto await_step = [&]() {
+      if (fine)
+        fine = __all_sync(kAll, mbar_wait_bounded(&full_r[u_slot], u_par, &abort_s, kWaitNs));
+      if (!fine) abort_s = 1;  // the others' waits end too
+    };
+    auto next_step = [&]() {
+      if (++u_slot == ST) {
+        u_slot = 0;
+        u_par ^= 1;
+      }
+    };
+    if (!mine && slice < p.slices) {
+#pragma unroll 1
+      for (int k = 0; k < n_slice; ++k) {
+        await_step();
+        if (lane == 0 && fine) mbar_arrive(&empty_r[u_slot]);
+        next_step();
+      }
+    }
 
     float oacc[C::MT][4];
 #pragma unroll
@@ -321,11 +389,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     float m_run = -INFINITY, l_run = 0.f, v_ref = 0.f;
 
     if (n_mine > 0) {
-      // ---- step records: id, mask and scales of 32 steps at a time, a batch
-      // ahead: ids 32 steps before their use, scales 16 before
+      // ---- step records: id, mask and scales of 8 steps at a time (a lane
+      // each), a batch ahead: ids 8 steps before their use, scales 4 before
       const int bps = p.bs_shift == 5 ? 1 : 0;
       auto fetch_id = [&](int k) -> int {  // of this warp's step k
-        if (k >= n_mine) return -1;
+        if (k >= n_mine || lane >= kBatch) return -1;
         const int blk = (step0 + k * p.slices) >> bps;
         return p.table[(size_t)s * p.max_blocks + blk];
       };
@@ -353,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         return m;
       };
       auto put = [&](int k, int id, float ks, float vs) {
-        meta[k & (kMeta - 1)] = Meta{id, mask_of(k, id), ks, vs};
+        if (lane < kBatch) meta[k & (kMeta - 1)] = Meta{id, mask_of(k, id), ks, vs};
       };
       auto scale_of = [&](const float *sc, int id) -> float {
         return id >= 0 ? __ldg(sc + (size_t)id * p.H + kvh) : 0.f;
@@ -361,67 +429,62 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
       int id_0 = fetch_id(lane);
       check_id(id_0);
       put(lane, id_0, 0.f, 0.f);
-      int id_n = fetch_id(32 + lane);
+      int id_n = fetch_id(kBatch + lane);
       float ks_n = 0.f, vs_n = 0.f;
       __syncwarp();
 
-      // ---- the copies of step k into its queue slot: a lane's bytes of 8 rows
-      // apart (K) or of rows 2c, 2c + 1, 8 + 2c, 9 + 2c (V), at fixed offsets from
-      // the step's first cell
-      const uint32_t row = (uint32_t)p.H * D;
-      const uint8_t *k_l = p.k_pool + (size_t)kvh * D + (size_t)g * row + 16 * c;
-      const uint8_t *v_l = p.v_pool + (size_t)kvh * D + (size_t)(2 * c) * row + C::VB * g;
-      uint32_t dst = ring_a + lane * 16;  // of the step to be issued
-      int i_slot = 0;
+      // ---- the copies of step k, by the ring's leader
       auto issue = [&](int k) {
-        if (k < n_mine) {
-          const Meta &mt = meta[k & (kMeta - 1)];
-          const uint32_t mask = mt.mask;
-          const int half = p.bs_shift == 5 ? ((step0 + k * p.slices) & 1) * kStep : 0;
-          // (a hole's step copies nothing, from a valid address)
-          const size_t base = (((size_t)max(mt.phys, 0) << p.bs_shift) + half) * row;
-          const uint32_t vdst = dst + kStep * D - lane * (16 - C::VB);
-          const uint8_t *ks = k_l + base, *vs = v_l + base;
-          if (mask == 0xffffu) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int j = 0; j < C::KP; ++j)
-                copy_async<16>(dst + (t * C::KP + j) * 512, ks + t * (8 * row) + 64 * j);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-              for (int j = 0; j < C::VP; ++j)
-                copy_async<C::VB>(vdst + (t * C::VP + j) * (32 * C::VB),
-                                  vs + ((t & 1) + 8 * (t >> 1)) * row + 128 * j);
+        if (!leader || !fine || k >= n_mine) return;
+        const Meta &mt = meta[k & (kMeta - 1)];
+        fine = __all_sync(kAll, mbar_wait_bounded(&empty_r[i_slot], i_par, &abort_s, kWaitNs));
+        if (!fine) {
+          abort_s = 1;  // the others' waits end too
+          return;
+        }
+        const uint32_t dst = ring_a + (uint32_t)(i_slot * p.stage_bytes);
+        uint64_t *bar = &full_r[i_slot];
+        const int half = p.bs_shift == 5 ? ((step0 + k * p.slices) & 1) * kStep : 0;
+        const long long cell = ((long long)mt.phys << p.bs_shift) + half;
+        const size_t row = (size_t)p.H * D;
+        if (mt.mask == 0u) {
+          if (lane == 0) mbar_arrive(bar);
+        } else if (p.copy == kRowwise) {
+          // lane: a row of K (0..15) or of V
+          const uint32_t bytes = (uint32_t)(min(p.hc, p.H - hg * p.hc) * D);
+          if (lane == 0) mbar_arrive_expect_tx(bar, 32 * bytes);
+          __syncwarp();
+          copy_bulk(dst + (lane >> 4) * (p.stage_bytes / 2) + (lane & 15) * p.pitch,
+                    (lane < 16 ? p.k_pool : p.v_pool) + (size_t)(cell + (lane & 15)) * row +
+                        (size_t)hg * p.hc * D,
+                    bytes, bar);
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(bar, 2 * kStep * p.pitch);
+          if (p.copy == kTensor) {
+            copy_tensor(dst, &p.map_k, (int)cell, bar);
+            copy_tensor(dst + p.stage_bytes / 2, &p.map_v, (int)cell, bar);
           } else {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int j = 0; j < C::KP; ++j)
-                copy_async<16>(dst + (t * C::KP + j) * 512, ks + t * (8 * row) + 64 * j,
-                               (mask >> (8 * t + g)) & 1u);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-              for (int j = 0; j < C::VP; ++j)
-                copy_async<C::VB>(vdst + (t * C::VP + j) * (32 * C::VB),
-                                  vs + ((t & 1) + 8 * (t >> 1)) * row + 128 * j,
-                                  (mask >> (2 * c + (t & 1) + 8 * (t >> 1))) & 1u);
-          }
-          dst += C::STAGE;
-          if (++i_slot == ST) {
-            i_slot = 0;
-            dst -= ST * C::STAGE;
+            copy_bulk(dst, p.k_pool + (size_t)cell * row, kStep * p.pitch, bar);
+            copy_bulk(dst + p.stage_bytes / 2, p.v_pool + (size_t)cell * row, kStep * p.pitch, bar);
           }
         }
-        copy_commit();
+        __syncwarp();
+        if (++i_slot == ST) {
+          i_slot = 0;
+          i_par ^= 1;
+        }
       };
-#pragma unroll
       for (int k = 0; k < ST - 1; ++k) issue(k);
       // scales of the first batch, once its copies are under way
-      meta[lane].ks = scale_of(p.k_scales, id_0);
-      meta[lane].vs = scale_of(p.v_scales, id_0);
+      if (lane < kBatch) {
+        meta[lane].ks = scale_of(p.k_scales, id_0);
+        meta[lane].vs = scale_of(p.v_scales, id_0);
+      }
+      if (ST - 1 > kBatch / 2) {  // the loop's first look is past this batch's scales
+        check_id(id_n);
+        ks_n = scale_of(p.k_scales, id_n);
+        vs_n = scale_of(p.v_scales, id_n);
+      }
       __syncwarp();
 
       // ---- the group's queries as A fragments: q / 2^e in high and low f16
@@ -456,40 +519,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         }
       }
 
-      uint32_t st = ring_a + lane * 16;  // of the step to be used
-      int u_slot = 0;
-      float v_inv = 0.f;                 // 1 / v_ref
+      float v_inv = 0.f;  // 1 / v_ref
 #pragma unroll 1
-      for (int k = 0; k < n_mine; ++k, st += C::STAGE) {
-        if (u_slot == ST) {
-          u_slot = 0;
-          st -= ST * C::STAGE;
-        }
-        ++u_slot;
+      for (int k = 0; k < n_mine; ++k) {
         const int ki = k + ST - 1;  // the step whose copies start now
-        if ((ki & 31) == 16) {
+        if ((ki & (kBatch - 1)) == kBatch / 2) {
           check_id(id_n);
           ks_n = scale_of(p.k_scales, id_n);
           vs_n = scale_of(p.v_scales, id_n);
-        } else if ((ki & 31) == 31) {
-          const int k0 = (ki & ~31) + 32;
+        } else if ((ki & (kBatch - 1)) == kBatch - 1) {
+          const int k0 = (ki & ~(kBatch - 1)) + kBatch;
           if (k0 < n_mine) {
             put(k0 + lane, id_n, ks_n, vs_n);
-            id_n = fetch_id(k0 + 32 + lane);
+            id_n = fetch_id(k0 + kBatch + lane);
           }
           __syncwarp();
         }
         issue(ki);
-        copy_wait<ST - 1>();
+        await_step();
         const Meta mt = meta[k & (kMeta - 1)];
-        if (mt.mask == 0u) continue;
+        const uint32_t st = ring_a + (uint32_t)(u_slot * p.stage_bytes);
+        uint64_t *done = &empty_r[u_slot];
+        next_step();
+        // (once a wait has run out nothing is freed either, so nothing is refilled)
+        if (mt.mask == 0u || !fine) {
+          __syncwarp();
+          if (lane == 0 && fine) mbar_arrive(done);
+          continue;
+        }
 
         // ---- scores
         uint4 kw[2][C::KP];
 #pragma unroll
         for (int j = 0; j < C::KP; ++j)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) kw[t][j] = lds16(st + (t * C::KP + j) * 512);
+          for (int t = 0; t < 2; ++t) kw[t][j] = lds16(st + k_at[t][j]);
         float sc[2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -511,23 +575,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
           for (int i = 0; i < 4; ++i) sc[t][i] = s0[i] + s1[i];
         }
         // V's first piece, on its way while the softmax runs
-        const uint32_t vt = st + kStep * D - lane * (16 - C::VB);
         uint32_t w[4][C::VB / 4];
         auto load_v = [&](int j) {
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const uint32_t at = vt + (t * C::VP + j) * (32 * C::VB);
             if constexpr (C::VB == 16) {
-              const uint4 u = lds16(at);
+              const uint4 u = lds16(st + v_at[t][j]);
               w[t][0] = u.x;
               w[t][1] = u.y;
               w[t][2] = u.z;
               w[t][3] = u.w;
             } else {
-              const uint2 u = lds8(at);
+              const uint2 u = lds8(st + v_at[t][j]);
               w[t][0] = u.x;
               w[t][1] = u.y;
             }
+            // positions that are not read: their codes may be anything, and a
+            // NaN times a probability of 0 would reach the row
+            if (mt.mask != 0xffffu && !((mt.mask >> (2 * c + (t & 1) + 8 * (t >> 1))) & 1u)) {
+#pragma unroll
+              for (int i = 0; i < C::VB / 4; ++i) w[t][i] = 0u;
+            }
+          }
+          if (j == C::VP - 1) {  // the step's last read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(done);
           }
         };
         load_v(0);
@@ -600,7 +672,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
           }
         }
       }
-      copy_wait<0>();
       l_run += __shfl_xor_sync(kAll, l_run, 1);
       l_run += __shfl_xor_sync(kAll, l_run, 2);
     }
@@ -615,8 +686,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     }
     // ---- warps that shared a KV head's steps: merged by the first of them
     if (p.slices > 1) {
-      float *own = reinterpret_cast<float *>(ring);  // [8 heads][D], then m[8], l[8] in meta
-      float2 *ml = reinterpret_cast<float2 *>(meta);
+      // every copy has landed and been read: the ring is scratch here
+      __syncthreads();
+      constexpr int OWN = 8 * D * 4;  // a warp's [8 heads][D]
+      float *own = reinterpret_cast<float *>(smem + warp * OWN);
+      float2 *ml = reinterpret_cast<float2 *>(meta);  // m, l of the 8 heads
       if (slice > 0) {
 #pragma unroll
         for (int m = 0; m < C::MT; ++m) {
@@ -629,9 +703,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
       if (slice == 0 && mine) {
         for (int w = 1; w < p.slices; ++w) {
           const int ow = warp + w * p.hc;
-          const float *oo = reinterpret_cast<const float *>(smem + ow * (ST * C::STAGE));
-          const float2 o_ml = reinterpret_cast<const float2 *>(
-              smem + kWarps * ST * C::STAGE + (size_t)ow * kMeta * sizeof(Meta))[g];
+          const float *oo = reinterpret_cast<const float *>(smem + ow * OWN);
+          const float2 o_ml = reinterpret_cast<const float2 *>(meta + (w * p.hc) * kMeta)[g];
           if (__any_sync(kAll, o_ml.x != -INFINITY || o_ml.y != 0.f)) {
             const float m_new = fmaxf(m_run, o_ml.x);
             const float f0 = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
@@ -651,6 +724,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
           }
         }
       }
+      // (ordered before the next segment's copies into the same bytes)
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
     }
     // ---- heads 2c and 2c + 1: dims 16 g + 2 m + (0, 1) of each 128-dim part
@@ -697,6 +772,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         if (s >= p.B) break;
         window_of(s, lo, hi);
       } while (hi <= lo);
+    }
+  }
+  if (!fine) {
+    if (lane == 0) report(p.status, MT_STATUS_BIT_TIMEOUT);
+    if (leader) {
+      // copies still in flight land before the CTA leaves
+      int never = 0;
+      for (int i = 0; i < ST; ++i)
+        mbar_wait_bounded(&full_r[i], i < i_slot ? i_par ^ 1 : i_par, &never, kWaitNs);
     }
   }
 }
@@ -857,6 +941,18 @@ mt_status make_plan(const mt_f8_attn_args *a, const char *where, Plan *pl) {
   p.hc = std::min(p.H, kWarps);
   p.n_hg = (p.H + p.hc - 1) / p.hc;
   p.slices = kWarps / p.hc;
+  // staging: the head group's part of a row; a whole row of 128-byte lines takes
+  // an odd number of them
+  const int row = p.hc * c.head_dim;
+  const bool cells32 = c.n_phys_blocks * c.block_size <= 0x7fffffffLL;  // a tensor copy's range
+  p.copy = p.n_hg > 1 ? kRowwise : row % 128 ? kWhole : cells32 ? kTensor : kRowwise;
+  p.pitch = p.copy == kRowwise ? row + 16 : p.copy == kTensor ? (row / 128 | 1) * 128 : row;
+  p.stage_bytes = (2 * kStep * p.pitch + 1023) / 1024 * 1024;
+  const int ring = (c.head_dim == 64    ? Cfg<64>::SMEM - Cfg<64>::META
+                    : c.head_dim == 128 ? Cfg<128>::SMEM - Cfg<128>::META
+                                        : Cfg<256>::SMEM - Cfg<256>::META) -
+                   1024;
+  p.stages = std::min(kMaxStages, ring / (p.slices * p.stage_bytes));
   const long long rows = (long long)p.B * p.n_hg;
   // a (sequence, head group) of up to 256 positions is one CTA's work: no
   // pieces and no second launch
@@ -873,6 +969,7 @@ template <int D, int DT>
 mt_status launch(const Plan &pl, cudaStream_t s) {
   auto kern = decode_f8_kernel<D, DT>;
   constexpr int smem = Cfg<D>::SMEM;
+  static_assert(Cfg<D>::SMEM - 1024 - Cfg<D>::META >= kWarps * 8 * D * 4, "the merge's scratch");
   mt_status st = kernel_smem(reinterpret_cast<const void *>(kern), smem,
                              "cudaFuncSetAttribute(f8 decode smem)", true);
   if (st != MT_OK) return st;
@@ -919,6 +1016,14 @@ extern "C" mt_status mt_paged_attn_decode_f8(const mt_f8_attn_args *a, void *wor
   pl.p.part_o = reinterpret_cast<float *>(ws + kHdrBytes);
   pl.p.part_ml = reinterpret_cast<float2 *>(
       pl.p.part_o + (size_t)pl.slots * pl.p.hc * pl.p.G * a->cache.head_dim);
+  if (pl.p.copy == kTensor) {
+    const long long cells = (long long)a->cache.n_phys_blocks * a->cache.block_size;
+    const size_t rb = (size_t)pl.p.H * a->cache.head_dim;
+    st = encode_pool_map_3d(&pl.p.map_k, pl.p.k_pool, cells, rb, pl.p.pitch / 128, kStep);
+    if (st != MT_OK) return st;
+    st = encode_pool_map_3d(&pl.p.map_v, pl.p.v_pool, cells, rb, pl.p.pitch / 128, kStep);
+    if (st != MT_OK) return st;
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = a->cache.head_dim == 64    ? launch_dt<64>(pl, a->dtype, s)
        : a->cache.head_dim == 128 ? launch_dt<128>(pl, a->dtype, s)
