@@ -169,8 +169,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# The current stream's handle without building a Stream object: 0.2 us against
+# 3 us a call. The public way where a torch build lacks it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -329,12 +336,13 @@ def mt_paged_attn_decode_static(args: mt_paged_attn_args, status=None, stream=No
            "mt_paged_attn_decode_static")
 
 
-def _ptr_here(t, dtypes, what: str) -> int | None:
+def _ptr_here(t, dtypes, what: str, here: int | None = None) -> int | None:
     """Address of a contiguous tensor of one of `dtypes` on the current device
-    (the calls launch there)."""
+    (`here`, where the calls launch)."""
     if t is None:
         return None
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    index = t.get_device()  # -1: host memory
+    if index < 0 or index != (torch.cuda.current_device() if here is None else here):
         raise ValueError(f"{what}: expected a tensor on the current CUDA device, got {t.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: unexpected dtype {t.dtype}")
@@ -375,16 +383,18 @@ def f8_cache(k_pool, v_pool, k_scales, v_scales, block_table, context_lens) -> m
 
 def _f8_rows(cache, k, v, q_start, what: str) -> tuple:
     """dtype, addresses and row count of a pair of dense row arrays."""
-    dt = _DTYPES.get(k.dtype)
-    n = k.shape[0]
-    if dt is None or v.dtype != k.dtype:
+    dtype, shape = k.dtype, k.shape
+    dt = _DTYPES.get(dtype)
+    if dt is None or v.dtype != dtype:
         raise ValueError(f"{what}: rows must be float32, float16 or bfloat16, both alike")
-    if k.shape != v.shape or k.numel() != n * cache.n_kv_heads * cache.head_dim:
+    n = shape[0]
+    if shape != v.shape or k.numel() != n * cache.n_kv_heads * cache.head_dim:
         raise ValueError(f"{what}: rows must be [n_tokens][n_kv_heads][head_dim], both alike")
-    if q_start.shape != (cache.n_seqs + 1,):
+    if q_start.dim() != 1 or q_start.numel() != cache.n_seqs + 1:
         raise ValueError(f"{what}: q_start must be [n_seqs + 1]")
-    own = (k.dtype,)
-    return dt, _ptr_here(k, own, what), _ptr_here(v, own, what), _ptr_here(q_start, _I32, what), n
+    own, here = (dtype,), (torch.cuda.current_device() if k.get_device() >= 0 else -1)
+    return (dt, _ptr_here(k, own, what, here), _ptr_here(v, own, what, here),
+            _ptr_here(q_start, _I32, what, here), n)
 
 
 def mt_kv_store_f8(cache: mt_f8_cache, k_new, v_new, q_start, status=None, stream=None) -> None:

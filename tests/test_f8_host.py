@@ -136,8 +136,11 @@ class Elsewhere:
     """A tensor's face on a device that is not the current one."""
 
     def __init__(self, t, index):
-        self._t, self.is_cuda, self.device = t, True, torch.device("cuda", index)
+        self._t, self.device = t, torch.device("cuda", index)
         self.dtype, self.shape = t.dtype, t.shape
+
+    def get_device(self):
+        return self.device.index
 
     def is_contiguous(self):
         return self._t.is_contiguous()
