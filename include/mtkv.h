@@ -369,7 +369,7 @@ typedef struct {
   int n_kv_heads;              /* 1 .. 256                                        */
   int head_dim;                /* 64, 128 or 256                                  */
   int block_size;              /* 16 or 32                                        */
-  int max_blocks;
+  int max_blocks;              /* max_blocks * block_size below 2^31 - 1023       */
   int64_t n_phys_blocks;
 } mt_f8_cache;
 

@@ -944,7 +944,8 @@ mt_status make_plan(const mt_f8_attn_args *a, const char *where, Plan *pl) {
   // staging: the head group's part of a row; a whole row of 128-byte lines takes
   // an odd number of them
   const int row = p.hc * c.head_dim;
-  const bool cells32 = c.n_phys_blocks * c.block_size <= 0x7fffffffLL;  // a tensor copy's range
+  const long long cells = c.n_phys_blocks * c.block_size;
+  const bool cells32 = cells > 0 && cells <= 0x7fffffffLL;  // a tensor map's range
   p.copy = p.n_hg > 1 ? kRowwise : row % 128 ? kWhole : cells32 ? kTensor : kRowwise;
   p.pitch = p.copy == kRowwise ? row + 16 : p.copy == kTensor ? (row / 128 | 1) * 128 : row;
   p.stage_bytes = (2 * kStep * p.pitch + 1023) / 1024 * 1024;

@@ -177,11 +177,12 @@ struct Walk {
 };
 
 __device__ __forceinline__ int tiles_of(const PrefillF8Params &p, int s, bool flag) {
-  const int q0 = p.q_start[s], q1 = p.q_start[s + 1], n = q1 - q0;
-  const bool bad = n < 0 || (n > 0 && (q0 < 0 || q1 > p.n_tok));
+  const int q0 = p.q_start[s], q1 = p.q_start[s + 1];
+  const bool bad = q1 < q0 || (q1 > q0 && (q0 < 0 || q1 > p.n_tok));
+  const int n = bad ? 0 : q1 - q0;
   if (flag && (bad || (n > 0 && (n > p.ctx[s] || p.ctx[s] > (p.max_blocks << p.bs_shift)))))
     report(p.status, MT_STATUS_BIT_DEVICE_CHECK);
-  return bad || n == 0 ? 0 : (n + p.tq - 1) / p.tq;
+  return (n + p.tq - 1) / p.tq;
 }
 
 // Tiles of all sequences, and the most chunks any of them has: whole warp.
@@ -376,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the converters work a chunk ahead and may sleep longer
   const unsigned nap = warp >= kConvWarp && warp < kMmaWarp ? 256 : 20;
   // Wait for a phase (bounded; false: it ran out, or another role gave up), by
-  // one thread, which sleeps between its polls: polling without a pause, the
-  // waiting warps executed a third of the CTA's instructions.
+  // one thread, which sleeps between its polls so that the waiting warps leave the
+  // issue slots to the others (naps of 0 to 256 ns take the same time).
   auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (mbar_try_wait(bar, parity & 1u)) return true;
     const uint64_t t0 = global_ns();

@@ -38,6 +38,7 @@ BAD_CACHE = [(dict(n_seqs=-1), 1), (dict(n_kv_heads=0), 1), (dict(max_blocks=-1)
              (dict(block_size=8), 2), (dict(n_kv_heads=257), 2), (dict(k_pool=None), 1),
              (dict(v_scales=None), 1), (dict(block_table=None), 1), (dict(context_lens=None), 1),
              (dict(k_pool=A + 8), 1), (dict(max_blocks=1 << 28), 2),
+             (dict(max_blocks=(1 << 27) - 1), 2), (dict(max_blocks=(1 << 26) - 1, block_size=32), 2),
              (dict(n_phys_blocks=1 << 31), 2)]
 
 

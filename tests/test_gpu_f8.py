@@ -216,6 +216,34 @@ def test_store_skips_holes_and_flags_bad_input(mt):
     check_cache(w)
 
 
+@pytest.mark.parametrize("n_seqs", [1, 31, 32, 33, 70, 1100])
+def test_store_finds_its_rows_among_any_number_of_sequences(mt, n_seqs):
+    rng = np.random.default_rng(15)
+    ctx = rng.integers(0, 50, n_seqs)
+    n = np.minimum(rng.integers(0, 3, n_seqs) * rng.integers(0, 40, n_seqs), ctx)
+    w = World(mt, 16, ctx, 1, 64, 16)
+    cache = w.upload()
+    q_start = np.concatenate([[0], np.cumsum(n)])
+    new = [rounded(rng.normal(size=(q_start[-1], 1, 64)), "f16") for _ in range(2)]
+    assert run_store(w, cache, new, q_start, "f16") == mt.MT_OK
+    for x, pool, sc in zip(new, w.pools, w.scales):
+        f8.store(pool, sc, x, w.table, w.ctx, q_start, 16)
+    check_cache(w)
+
+
+@pytest.mark.parametrize("q_start", [[0, 5, -2 ** 31, 7], [0, 5, 2 ** 31 - 1, 9],
+                                     [-2 ** 31, 2 ** 31 - 1, 4, 4]])
+def test_row_bounds_at_the_ends_of_the_integers(mt, q_start):
+    w = World(mt, 17, [20, 20, 20], 2, 64, 16)
+    cache = w.upload()
+    new = [w.rng.normal(size=(7, 2, 64)).astype(np.float32) for _ in range(2)]
+    assert run_store(w, cache, new, q_start, "f32") == mt.MT_ERR_DEVICE_CHECK
+    q, qd = w.q(7, 2, "f32")
+    out, _ = run_prefill(w, cache, qd, q_start, "f32", want_status=mt.MT_ERR_DEVICE_CHECK)
+    good = 5 if q_start[1] == 5 else 0
+    assert out[:good].isfinite().all() and out[good:].isnan().all()
+
+
 # -------------------------------------------------------------------- load
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
@@ -779,3 +807,33 @@ def test_prefill_captured_into_a_graph_and_on_two_streams(mt):
         torch.cuda.synchronize()
         assert torch.equal(out, first)
         compare(sets[1][2], sets[1][3], *oracle(w, sets[1][4], q_start=qs), "f16")
+
+
+@pytest.mark.parametrize("max_blocks", [0, 2, 40])
+def test_a_cache_without_blocks(mt, max_blocks):
+    pool = torch.empty(0, 16, 2, 64, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(0, 2, device="cuda")
+    ctx = np.array([0, min(max_blocks * 16, 500)], dtype=np.int32)
+    table = torch.full((2, max_blocks), -1, dtype=torch.int32, device="cuda")
+    cache = mt.f8_cache(pool, pool, sc, sc, table, dev(ctx))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_start = dev(np.array([0, 0, min(ctx[1], 3)], dtype=np.int32))
+    x = [torch.randn(3, 2, 64, device="cuda") for _ in range(2)]
+    mt.mt_kv_store_f8(cache, *x, q_start, status=status)
+    y = [torch.full((3, 2, 64), 7.0, device="cuda") for _ in range(2)]
+    mt.mt_kv_load_f8(cache, *y, q_start, status=status)
+    assert mt.mt_check_device_status(status) == mt.MT_OK
+    for call, rows, kw in (("decode", 2, {}), ("prefill", 3, {"q_start": q_start})):
+        q = torch.randn(rows, 4, 64, device="cuda")
+        out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        args = mt.f8_attn_args(cache, q, out, scale=0.1, lse=lse, **kw)
+        size = getattr(mt, f"mt_paged_attn_{call}_f8_workspace_bytes")(args)
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        getattr(mt, f"mt_paged_attn_{call}_f8")(args, ws)
+        assert mt.mt_check_device_status(ws) == mt.MT_OK
+        n = rows if call == "decode" or max_blocks else 0   # rows that a sequence has
+        assert (out[:n] == 0).all() and lse[:n].isneginf().all()
+        assert (out[n:] == 7.0).all()
+    n = 3 if max_blocks else 0
+    for t in y:
+        assert (t[:n] == 0).all() and (t[n:] == 7.0).all()
