@@ -11,7 +11,10 @@
 // head_dim operations). Design:
 //  * Work is the stream of all (sequence, head group, 16-position step)
 //    units, cut into equal ranges, one per CTA; every CTA derives its range
-//    from the context lengths. A CTA's warps take the KV heads of the same
+//    from the context lengths. Going over to the next (sequence, head group)
+//    costs a CTA the time of about 5 steps (the ring runs empty), so each
+//    counts that many more (without: 118 for 115 us with 64 sequences, 17.8 for
+//    15.5 us with 8 short ones; 3 or 8 steps instead: within 1 %). A CTA's warps take the KV heads of the same
 //    steps (and, with few KV heads, interleaved steps), so the lines they
 //    read together form whole blocks of the pool.
 //  * The cells of a step, all heads, arrive by one bulk copy each of K and V
@@ -36,7 +39,11 @@
 //    (running maximum up to 2^8 behind) their f16 stay below 2^15 and a
 //    probability of 1 has 2^31 steps below it.
 //  * Partial results of a (CTA, sequence, head group) are merged by a second
-//    kernel, a CTA per (sequence, query head).
+//    kernel.
+// Measured: Llama-3 heads (8 of 128, groups of 4), 64 sequences of 512..16384
+// positions 111 us (610 MB, 5.5 TB/s: 5 us until the first bytes are used, CTAs
+// that end between 87 and 103 us, 4 us of merging); 16 of 32768 at 4 heads of 256
+// 160 us (6.4 TB/s); 8 windows of 3 heads of 64, float32, 14.6 us (latency).
 #include <limits.h>
 #include <math.h>
 
@@ -59,7 +66,8 @@ constexpr int kBatch = 8;           // step records read at a time
 constexpr int kMeta = 2 * kBatch;   // step records per warp
 constexpr int kMaxStages = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMinSteps = 8;        // steps of a CTA's range, at least
+constexpr int kMinSteps = 4;        // units of a CTA's range, at least (8: 8 short windows 15.2 for 14.6 us)
+constexpr int kSegSteps = 5;        // what starting a (sequence, head group) costs, in steps
 constexpr int kHdrBytes = 256;      // status word and padding at the workspace's start
 
 // How a step's cells are copied: all rows as one tensor copy (rows of whole
@@ -145,6 +153,10 @@ __device__ __forceinline__ int steps_of(int lo, int hi) {
   return hi > lo ? (hi - 1) / kStep - lo / kStep + 1 : 0;
 }
 
+// Units of a sequence in the stream: its steps, behind kSegSteps that stand for the
+// time a CTA takes to go over to it.
+__device__ __forceinline__ int units_of(int steps) { return steps ? steps + kSegSteps : 0; }
+
 __device__ __forceinline__ long long warp_incl(long long v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -155,15 +167,15 @@ __device__ __forceinline__ long long warp_incl(long long v) {
   return v;
 }
 
-// Steps of all sequences before s, and of all sequences: the whole warp takes part.
-__device__ __forceinline__ void count_steps(const DecodeParams &p, int s, long long &before,
+// Units of all sequences before s, and of all sequences: the whole warp takes part.
+__device__ __forceinline__ void count_units(const DecodeParams &p, int s, long long &before,
                                             long long &total) {
   const int lane = threadIdx.x & 31;
   before = total = 0;
   for (int t = lane; t < p.B; t += 32) {
     int lo, hi;
     window(p, t, lo, hi);
-    const int n = steps_of(lo, hi);
+    const int n = units_of(steps_of(lo, hi));
     total += n;
     if (t < s) before += n;
   }
@@ -285,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
   // ---- this CTA's range of the stream (sequence, head group, step)
   long long r0 = 0, r1 = 0;
   int s = 0, hg = 0;       // where it starts
-  long long skip = 0;      // steps of (s, hg) before the range
+  long long skip = 0;      // units of (s, hg) before the range
   int w_lo = 0, w_hi = 0;  // sequence `lane`'s window (B <= 32)
   if (p.whole) {
     s = blockIdx.x / p.n_hg;
@@ -297,11 +309,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     if (p.B <= 32) {
       // every window is loaded once, and kept: lane t has sequence t's
       if (lane < p.B) window(p, lane, w_lo, w_hi);
-      k = steps_of(w_lo, w_hi);
+      k = units_of(steps_of(w_lo, w_hi));
       incl = warp_incl(k);
       total = __shfl_sync(kAll, incl, 31);
     } else {
-      count_steps(p, 0, before, total);
+      count_units(p, 0, before, total);
     }
     total *= p.n_hg;
     const int n = ctas_used(p, total);
@@ -317,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         if (b0 + lane < p.B) {
           int lo, hi;
           window(p, b0 + lane, lo, hi);
-          k = steps_of(lo, hi);
+          k = units_of(steps_of(lo, hi));
         }
         incl = warp_incl(k);
       }
@@ -350,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
     int lo, hi;
     window_of(s, lo, hi);
     const int n_all = steps_of(lo, hi);
-    const int a = (int)skip;
-    const int b = (int)min((long long)n_all, skip + left);
+    const int a = max((int)skip - kSegSteps, 0);
+    const int b = (int)min((long long)n_all, max(skip + left - kSegSteps, 0LL));
     const int kvh = hg * p.hc + head_l;
     const bool mine = slice < p.slices && kvh < p.H;
     // steps of this warp's slice, and its own (none without a head)
@@ -427,6 +439,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
         return id >= 0 ? __ldg(sc + (size_t)id * p.H + kvh) : 0.f;
       };
       int id_0 = fetch_id(lane);
+      // (the queries' loads are on their way while the first ids are)
+      const bool row_ok = g < p.G;
+      const size_t qrow = ((size_t)s * p.Hq + (size_t)kvh * p.G + (row_ok ? g : 0)) * D;
+      float4 x[C::KS];
+#pragma unroll
+      for (int j = 0; j < C::KS; ++j) {
+          const int d = (j >> 2) * 64 + 16 * c + 4 * (j & 3);
+          x[j] = row_ok ? load4<DT>(p.q, qrow + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
       check_id(id_0);
       put(lane, id_0, 0.f, 0.f);
       int id_n = fetch_id(kBatch + lane);
@@ -492,15 +513,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
       uint32_t qa[C::KS][4];
       float qfac;  // the row's factor on scores, 2^e * scale * log2(e)
       {
-        const bool row_ok = g < p.G;
-        const size_t qrow =
-            ((size_t)s * p.Hq + (size_t)kvh * p.G + (row_ok ? g : 0)) * D;
         float qmax = 0.f;
-        float4 x[C::KS];
 #pragma unroll
         for (int j = 0; j < C::KS; ++j) {
-          const int d = (j >> 2) * 64 + 16 * c + 4 * (j & 3);
-          x[j] = row_ok ? load4<DT>(p.q, qrow + d) : make_float4(0.f, 0.f, 0.f, 0.f);
           qmax = fmaxf(fmaxf(qmax, fmaxf(fabsf(x[j].x), fabsf(x[j].y))),
                        fmaxf(fabsf(x[j].z), fabsf(x[j].w)));
         }
@@ -729,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
       __syncthreads();
     }
     // ---- heads 2c and 2c + 1: dims 16 g + 2 m + (0, 1) of each 128-dim part
-    if (mine && slice == 0) {
+    if (mine && slice == 0 && (b > a || p.whole)) {
       const bool done = a == 0 && b == n_all;  // the whole (sequence, head group)
       const float l0 = __shfl_sync(kAll, l_run, 8 * c), l1 = __shfl_sync(kAll, l_run, 8 * c + 4);
       const size_t slot = (size_t)slot_cta + (size_t)s * p.n_hg + hg;
@@ -762,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
       }
     }
     if (p.whole) break;
-    left -= b - a;
+    left -= units_of(n_all) - skip;
     skip = 0;
     if (++hg == p.n_hg) {
       hg = 0;
@@ -787,27 +802,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::CTAS)
 
 // Merge the partial results of split (sequence, head group)s: MW warps for each
 // (sequence, query head) take its pieces in turn, then merge through shared
-// memory. One warp when there are rows enough for every SM and few pieces a row,
-// else all eight of a CTA. Sequences that see nothing get 0 and -infinity here;
-// those that one CTA finished are left alone.
-constexpr int kMergeWarps = 8;
+// memory. A CTA has one row, or with MW = 1 kMergeRows. Sequences that see
+// nothing get 0 and -infinity here; those that one CTA finished are left alone.
+constexpr int kMergeRows = 8;
+constexpr int merge_threads(int mw) { return 32 * (mw == 1 ? kMergeRows : mw); }
 
 template <int D, int DT, int MW>
-__global__ void __launch_bounds__(32 * kMergeWarps)
+__global__ void __launch_bounds__(merge_threads(MW))
     merge_f8_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int DV = D / 32;
   __shared__ float o_s[MW > 1 ? MW : 1][MW > 1 ? D : 1];
   __shared__ float2 ml_s[MW];
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wi = warp % MW;  // of this row's warps
-  const int row = blockIdx.x * (kMergeWarps / MW) + warp / MW;
+  const int wi = MW == 1 ? 0 : warp;  // of this row's warps
+  const int row = MW == 1 ? blockIdx.x * kMergeRows + warp : blockIdx.x;
   const bool live = row < p.B * p.Hq;
   const int s = live ? row / p.Hq : 0, h = live ? row % p.Hq : 0;
   const int kvh = h / p.G, hg = kvh / p.hc;
   // lengths and windows are inputs: read before the decode kernel has ended
   long long before, total;
-  count_steps(p, s, before, total);
+  count_units(p, s, before, total);
   int lo, hi;
   window(p, s, lo, hi);
   const int n_all = steps_of(lo, hi);
@@ -815,7 +830,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   if (n_all > 0) {
     total *= p.n_hg;
     const int n = ctas_used(p, total);
-    const long long u0 = before * p.n_hg + (long long)hg * n_all, u1 = u0 + n_all - 1;
+    const long long u0 = before * p.n_hg + (long long)hg * units_of(n_all) + kSegSteps;
+    const long long u1 = u0 + n_all - 1;
     // CTA i holds units [total i / n, total (i + 1) / n)
     c0 = (int)(((u0 + 1) * n - 1) / total);
     c1 = (int)(((u1 + 1) * n - 1) / total);
@@ -829,7 +845,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll
   for (int e = 0; e < DV; ++e) acc[e] = 0.f;
   const size_t slot0 = (size_t)s * p.n_hg + hg;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = c0 + wi; i <= c1; i += MW) {
     const size_t rec = (slot0 + i) * per + hin;
     const float2 ml = __ldcg(p.part_ml + rec);
@@ -977,12 +993,16 @@ mt_status launch(const Plan &pl, cudaStream_t s) {
   st = cuda_check(launch_pdl(kern, dim3((unsigned)pl.ctas), dim3(kThreads), smem, s, pl.p),
                   "f8 decode launch");
   if (st != MT_OK || pl.p.whole) return st;
-  // pieces a row: the grid's CTAs over the rows' head groups, at the least
-  const long long rows = (long long)pl.p.B * pl.p.Hq;
-  const bool few = pl.ctas <= 8LL * pl.p.B * pl.p.n_hg;
-  auto merge = few ? merge_f8_kernel<D, DT, 1> : merge_f8_kernel<D, DT, kMergeWarps>;
-  const long long grid = few ? (rows + kMergeWarps - 1) / kMergeWarps : rows;
-  return cuda_check(launch_pdl(merge, dim3((unsigned)grid), dim3(32 * kMergeWarps), 0, s, pl.p),
+  // Warps of a row by its pieces, which are the grid's CTAs over the (sequence, head
+  // group)s on average: of the Llama-3 heads, 64 sequences (4.8 pieces) took 111.8
+  // us with two warps and 114.7 with one, 256 sequences (1.2) 119.9 and 112.9.
+  const long long groups = (long long)pl.p.B * pl.p.n_hg, rows = (long long)pl.p.B * pl.p.Hq;
+  const int mw = pl.ctas <= 2 * groups ? 1 : pl.ctas <= 8 * groups ? 2 : 8;
+  auto merge = mw == 1   ? merge_f8_kernel<D, DT, 1>
+               : mw == 2 ? merge_f8_kernel<D, DT, 2>
+                         : merge_f8_kernel<D, DT, 8>;
+  const long long grid = mw == 1 ? (rows + kMergeRows - 1) / kMergeRows : rows;
+  return cuda_check(launch_pdl(merge, dim3((unsigned)grid), dim3(merge_threads(mw)), 0, s, pl.p),
                     "f8 decode merge launch");
 }
 

@@ -347,6 +347,18 @@ def test_decode_short_table_takes_one_launch_with_the_same_result(mt):
     compare(*run_decode(w, w.upload(), qd, "f32"), *want, "f32")
 
 
+@pytest.mark.parametrize("n_seqs", [1, 3, 32, 40, 200, 700])
+@pytest.mark.parametrize("h,d", [(1, 64), (11, 64), (8, 128)])
+def test_decode_splits_any_number_of_sequences(mt, n_seqs, h, d):
+    rng = np.random.default_rng(33)
+    ctx = rng.integers(0, 40, n_seqs) * rng.integers(0, 2 + 600 // n_seqs, n_seqs)
+    w = World(mt, 34, ctx, h, d, 16, max_blocks=max(17, -(-int(ctx.max()) // 16)))
+    cache = w.upload()
+    q, qd = w.q(n_seqs, 1, "f16")
+    out, lse = run_decode(w, cache, qd, "f16")
+    compare(out, lse, *oracle(w, q), "f16")
+
+
 def test_decode_is_the_same_every_time(mt):
     w = World(mt, 34, [3000, 40, 800], 2, 128, 16)
     cache = w.upload()
