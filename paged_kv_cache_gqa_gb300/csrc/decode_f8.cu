@@ -14,9 +14,10 @@
 //    from the context lengths. Going over to the next (sequence, head group)
 //    costs a CTA the time of about 5 steps (the ring runs empty), so each
 //    counts that many more (without: 118 for 115 us with 64 sequences, 17.8 for
-//    15.5 us with 8 short ones; 3 or 8 steps instead: within 1 %). A CTA's warps take the KV heads of the same
-//    steps (and, with few KV heads, interleaved steps), so the lines they
-//    read together form whole blocks of the pool.
+//    15.5 us with 8 short ones; 3 or 8 steps instead: within 1 %). A CTA's
+//    warps take the KV heads of the same steps (and, with few KV heads,
+//    interleaved steps), so the lines they read together form whole blocks of
+//    the pool.
 //  * The cells of a step, all heads, arrive by one bulk copy each of K and V
 //    (tensor copies with the 128-byte swizzle where rows are whole 128-byte
 //    lines, so that the lanes' reads spread over the banks), into a ring that the
@@ -66,7 +67,7 @@ constexpr int kBatch = 8;           // step records read at a time
 constexpr int kMeta = 2 * kBatch;   // step records per warp
 constexpr int kMaxStages = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMinSteps = 4;        // units of a CTA's range, at least (8: 8 short windows 15.2 for 14.6 us)
+constexpr int kMinSteps = 4;        // units of a CTA's range, at least (8: 15.2 for 14.6 us below)
 constexpr int kSegSteps = 5;        // what starting a (sequence, head group) costs, in steps
 constexpr int kHdrBytes = 256;      // status word and padding at the workspace's start
 

@@ -13,8 +13,8 @@
 // from floor(q_start[s] / bs) + 2 s on, and a warp finds its sequence by a
 // search over q_start: with up to 32 sequences one round trip, a lane each. The
 // rows are on their way before the block's id has come. Bound: HBM for prompts
-// (139 MB of f16 prompts, 8 heads of 128, in 26.5 us: 5.25 TB/s; their float32
-// form in 41.2 us: 5.63 TB/s), the call's latency for a decode step.
+// (139 MB of f16 prompts, 8 heads of 128, in 26.1 us: 5.33 TB/s; their float32
+// form in 40.3 us: 5.76 TB/s), the call's latency for a decode step.
 //
 // Load. y = code * scale, each row's block looked up once per tile of rows.
 // Bound: HBM.
@@ -43,7 +43,8 @@ struct StoreParams {
 };
 
 template <int D, int BS, int DT>
-__global__ void __launch_bounds__(kThreads) store_f8_kernel(const __grid_constant__ StoreParams p) {
+__global__ void __launch_bounds__(kThreads, DT == MT_F32 ? 2 : 4)
+    store_f8_kernel(const __grid_constant__ StoreParams p) {
   constexpr int LPR = D / 8;                           // lanes per row, 8 values each
   constexpr int RPP = 32 / LPR;                        // rows per pass of a warp
   constexpr int PASSES = BS / RPP;                     // passes of one warp over a block
@@ -179,23 +180,24 @@ __global__ void __launch_bounds__(kThreads) store_f8_kernel(const __grid_constan
     }
   }
   // x / s: a power of two that pow2_scale gave is inverted exactly; a kept
-  // scale of another kind, which a caller may have written, divides
+  // scale of another kind, which a caller may have written, divides. With s = 0
+  // every finite value is 0, and an infinity keeps its saturated code.
   const bool pow2 = (__float_as_uint(s_new) & 0x7fffffu) == 0 && s_new >= 1.17549435e-38f &&
                     s_new <= 1.329228e36f;
-  const float inv = s_new > 0.f ? (pow2 ? f8::pow2_inv(s_new) : 0.f) : 0.f;
+  const float inv = pow2 ? f8::pow2_inv(s_new) : 1.f;
+  const bool divide = !pow2 && s_new > 0.f;
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const int r = (sub * NP + k) * RPP + r_lane;
     if (r < a || r >= z) continue;
     float f[8];
     v[k].get(f);
-    if (pow2 || !(s_new > 0.f)) {
-      // s_new == 0: every finite value is 0; an infinity keeps its saturated code
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = fabsf(f[i]) == INFINITY ? f[i] : f[i] * inv;
-    } else {
+    if (divide) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] /= s_new;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= inv;
     }
     uint2 w;
     w.x = f8::to_code4(f[0], f[1], f[2], f[3]);
