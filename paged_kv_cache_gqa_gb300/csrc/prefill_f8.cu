@@ -408,6 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&u_free[k]);
     return un.id >= 0;
   };
+  // Unit i has been found (or there is no such): no wait.
+  auto unit_there = [&](int i) -> bool {
+    return __all_sync(kAll, mbar_try_wait(&u_full[i & (kUnitSlots - 1)], (i / kUnitSlots) & 1));
+  };
   // The next unit from number i on that has chunks; i moves past it.
   auto live_unit = [&](int &i, Unit &un) -> bool {
 #pragma unroll 1
@@ -503,9 +507,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_scales(un.h);
     }
     while (have && fine) {
-      // the unit after this one
+      // The unit after this one that has chunks, if the scheduler has found it by
+      // now. (It runs no further than two units past the one whose products it
+      // issues, so behind units without chunks it may still need this one's.)
       Unit nx = un;
-      const bool have2 = live_unit(iu, nx);
+      bool have2 = false, known = false;
+#pragma unroll 1
+      while (!known && unit_there(iu)) {
+        have2 = next_unit(iu, nx);
+        if (have2) {
+          ++iu;
+          known = have2 = nx.ce > nx.cb;
+        } else {
+          known = true;  // there is none
+        }
+      }
       for (int c = un.cb; c < un.ce; ++c, ++g) {
         const int st = g % ST;
         const bool more = c + 1 < un.ce;
@@ -569,9 +585,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_proxy_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
+        if (!more && !known) break;
         ids = check_id(raw1);
         load(h1, c1, chunk1, ids);
         load_scales(h1);
+      }
+      if (!known && fine) {
+        ++g;  // (left the loop at its last chunk)
+        have2 = live_unit(iu, nx);
+        if (have2) {
+          ids = check_id(fetch_ids(nx.s, nx.c, nx.cb));
+          load(nx.h, nx.c, nx.cb, ids);
+          load_scales(nx.h);
+        }
       }
       un = nx;
       have = have2;

@@ -351,6 +351,22 @@ def _ptr_here(t, dtypes, what: str, here: int | None = None) -> int | None:
     return t.data_ptr()
 
 
+def _scratch_here(t, what: str, here: int) -> int | None:
+    """The same for a workspace or a status word, of any dtype."""
+    if t is None or isinstance(t, int):
+        return t
+    return _ptr_here(t, (t.dtype,), what, here)
+
+
+def _here(descriptor, what: str) -> int:
+    """The current device, which has to be the one of the descriptor's tensors."""
+    here = torch.cuda.current_device()
+    if getattr(descriptor, "_device", here) != here:
+        raise ValueError(f"{what}: the cache's tensors are on device {descriptor._device}, "
+                         f"the current CUDA device is {here}")
+    return here
+
+
 _I32 = (torch.int32,)
 _F32 = (torch.float32,)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -377,11 +393,12 @@ def f8_cache(k_pool, v_pool, k_scales, v_scales, block_table, context_lens) -> m
     c.context_lens = _ptr_here(context_lens, _I32, "context_lens")
     c.n_seqs, c.max_blocks = block_table.shape
     c.n_kv_heads, c.head_dim, c.block_size, c.n_phys_blocks = hkv, d, bs, n_phys
+    c._device = k_pool.get_device()
     c._tensors = (k_pool, v_pool, k_scales, v_scales, block_table, context_lens)
     return c
 
 
-def _f8_rows(cache, k, v, q_start, what: str) -> tuple:
+def _f8_rows(cache, k, v, q_start, what: str, here: int) -> tuple:
     """dtype, addresses and row count of a pair of dense row arrays."""
     dtype, shape = k.dtype, k.shape
     dt = _DTYPES.get(dtype)
@@ -392,7 +409,7 @@ def _f8_rows(cache, k, v, q_start, what: str) -> tuple:
         raise ValueError(f"{what}: rows must be [n_tokens][n_kv_heads][head_dim], both alike")
     if q_start.dim() != 1 or q_start.numel() != cache.n_seqs + 1:
         raise ValueError(f"{what}: q_start must be [n_seqs + 1]")
-    own, here = (dtype,), (torch.cuda.current_device() if k.get_device() >= 0 else -1)
+    own = (dtype,)
     return (dt, _ptr_here(k, own, what, here), _ptr_here(v, own, what, here),
             _ptr_here(q_start, _I32, what, here), n)
 
@@ -401,20 +418,25 @@ def mt_kv_store_f8(cache: mt_f8_cache, k_new, v_new, q_start, status=None, strea
     """Quantise rows into the 8-bit cache: the rows of sequence s,
     q_start[s] .. q_start[s+1]-1, become its last positions. k_new, v_new
     [n_tokens][n_kv_heads][head_dim] of float32, float16 or bfloat16."""
-    dt, k, v, qs, n = _f8_rows(cache, k_new, v_new, q_start, "mt_kv_store_f8")
-    _check(lib().mt_kv_store_f8(ctypes.byref(cache), dt, k, v, qs, n, _ptr(status),
-                                _stream(stream)), "mt_kv_store_f8")
+    here = _here(cache, "mt_kv_store_f8")
+    dt, k, v, qs, n = _f8_rows(cache, k_new, v_new, q_start, "mt_kv_store_f8", here)
+    _check(lib().mt_kv_store_f8(ctypes.byref(cache), dt, k, v, qs, n,
+                                _scratch_here(status, "status", here), _stream(stream)),
+           "mt_kv_store_f8")
 
 
 def mt_kv_load_f8(cache: mt_f8_cache, k_out, v_out, q_start, pos0=None, status=None,
                   stream=None) -> None:
     """Read rows of the 8-bit cache back into k_out, v_out: row j of sequence s
     is position pos0[s] + j, or without pos0 its last positions."""
-    dt, k, v, qs, n = _f8_rows(cache, k_out, v_out, q_start, "mt_kv_load_f8")
+    here = _here(cache, "mt_kv_load_f8")
+    dt, k, v, qs, n = _f8_rows(cache, k_out, v_out, q_start, "mt_kv_load_f8", here)
     if pos0 is not None and pos0.shape != (cache.n_seqs,):
         raise ValueError("mt_kv_load_f8: pos0 must be [n_seqs]")
-    _check(lib().mt_kv_load_f8(ctypes.byref(cache), dt, k, v, qs, _ptr_here(pos0, _I32, "pos0"),
-                               n, _ptr(status), _stream(stream)), "mt_kv_load_f8")
+    _check(lib().mt_kv_load_f8(ctypes.byref(cache), dt, k, v, qs,
+                               _ptr_here(pos0, _I32, "pos0", here), n,
+                               _scratch_here(status, "status", here), _stream(stream)),
+           "mt_kv_load_f8")
 
 
 def f8_attn_args(cache: mt_f8_cache, q, out, *, scale, q_start=None, spans=None, kv_map=None,
@@ -440,6 +462,7 @@ def f8_attn_args(cache: mt_f8_cache, q, out, *, scale, q_start=None, spans=None,
     a.q_start, a.spans = _ptr_here(q_start, _I32, "q_start"), _ptr_here(spans, _I32, "spans")
     a.kv_map = _ptr_here(kv_map, _I32, "kv_map")
     a.n_tokens, a.n_heads, a.scale = n, hq, float(scale)
+    a._device = getattr(cache, "_device", q.get_device())
     a._tensors = (cache, q, out, lse, q_start, spans, kv_map)
     return a
 
@@ -450,9 +473,11 @@ def mt_paged_attn_decode_f8_workspace_bytes(args: mt_f8_attn_args) -> int:
 
 def mt_paged_attn_decode_f8(args: mt_f8_attn_args, workspace, stream=None) -> None:
     """Decode attention over the 8-bit cache, one query per sequence."""
+    here = _here(args, "mt_paged_attn_decode_f8")
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().mt_paged_attn_decode_f8(ctypes.byref(args), _ptr(workspace), nbytes,
-                                         _stream(stream)), "mt_paged_attn_decode_f8")
+    ws = _scratch_here(workspace, "workspace", here)
+    _check(lib().mt_paged_attn_decode_f8(ctypes.byref(args), ws, nbytes, _stream(stream)),
+           "mt_paged_attn_decode_f8")
 
 
 def mt_paged_attn_prefill_f8_workspace_bytes(args: mt_f8_attn_args) -> int:
@@ -461,9 +486,11 @@ def mt_paged_attn_prefill_f8_workspace_bytes(args: mt_f8_attn_args) -> int:
 
 def mt_paged_attn_prefill_f8(args: mt_f8_attn_args, workspace, stream=None) -> None:
     """Multi-query (prefill) attention over the 8-bit cache."""
+    here = _here(args, "mt_paged_attn_prefill_f8")
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().mt_paged_attn_prefill_f8(ctypes.byref(args), _ptr(workspace), nbytes,
-                                          _stream(stream)), "mt_paged_attn_prefill_f8")
+    ws = _scratch_here(workspace, "workspace", here)
+    _check(lib().mt_paged_attn_prefill_f8(ctypes.byref(args), ws, nbytes, _stream(stream)),
+           "mt_paged_attn_prefill_f8")
 
 
 def _moves_array(moves):

@@ -161,3 +161,14 @@ def test_binding_checks_device_dtype_and_layout(mt, monkeypatch):
         mt._ptr_here(Elsewhere(t.half(), 0), f32, "x")
     with pytest.raises(ValueError, match="contiguous"):
         mt._ptr_here(Elsewhere(t.t(), 0), f32, "x")
+    with pytest.raises(ValueError, match="workspace"):
+        mt._scratch_here(Elsewhere(t, 1), "workspace", 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        mt._scratch_here(Elsewhere(t[:, ::2], 0), "workspace", 0)
+    c = cache_of(mt)
+    assert mt._here(c, "x") == 0
+    c._device = 1
+    for call in (lambda: mt.mt_kv_store_f8(c, t, t, t), lambda: mt.mt_kv_load_f8(c, t, t, t),
+                 lambda: mt.mt_paged_attn_decode_f8(c, t), lambda: mt.mt_paged_attn_prefill_f8(c, t)):
+        with pytest.raises(ValueError, match="on device 1"):
+            call()

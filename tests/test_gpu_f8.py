@@ -660,6 +660,21 @@ def test_prefill_many_units_a_cta(mt, dt, d):
     assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("live", [[0], [0, 1, 2, 60, 61, 199], [199], []])
+def test_prefill_long_runs_of_rows_that_see_nothing(mt, dt, live):
+    # 200 sequences x 8 heads of one query each: a CTA has about ten units, most of
+    # them without a position to read
+    w = World(mt, 51, [20 + 7 * (s % 30) for s in range(200)], 8, 64, 16)
+    cache = w.upload()
+    q, qd = w.q(200, 1, dt)
+    spans = np.zeros((200, 2), dtype=np.int32)
+    spans[live] = 0, 1000
+    out, lse = run_prefill(w, cache, qd, starts([1] * 200), dt, spans=spans)
+    want, want_lse = oracle(w, q, q_start=starts([1] * 200), spans=spans)
+    compare(out, lse, want, want_lse, dt)
+
+
 def test_prefill_window_far_from_the_start(mt):
     # chunks before every query's window are not needed at all
     ctx, n = [1500, 900], [20, 150]
