@@ -525,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = un.cb; c < un.ce; ++c, ++g) {
         const int st = g % ST;
         const bool more = c + 1 < un.ce;
-        const int s1 = more ? un.s : nx.s, h1 = more ? un.h : nx.h;
-        const int c1 = more || have2 ? (more ? un.c : nx.c) : 0;  // 0: nothing to load
-        const int chunk1 = more ? c + 1 : nx.cb;
-        const int raw1 = fetch_ids(s1, c1, chunk1);
+        int h1 = more ? un.h : nx.h;
+        int c1 = more ? un.c : have2 ? nx.c : 0;  // 0: nothing to load
+        int chunk1 = more ? c + 1 : nx.cb;
+        int raw1 = fetch_ids(more ? un.s : nx.s, c1, chunk1);
         if (g >= ST && !wait(&empty[st], g / ST - 1)) {
           fine = false;
           break;
@@ -585,19 +585,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_proxy_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
-        if (!more && !known) break;
+        if (!more && !known) {
+          have2 = live_unit(iu, nx);
+          h1 = nx.h;
+          c1 = have2 ? nx.c : 0;
+          chunk1 = nx.cb;
+          raw1 = fetch_ids(nx.s, c1, chunk1);
+        }
         ids = check_id(raw1);
         load(h1, c1, chunk1, ids);
         load_scales(h1);
-      }
-      if (!known && fine) {
-        ++g;  // (left the loop at its last chunk)
-        have2 = live_unit(iu, nx);
-        if (have2) {
-          ids = check_id(fetch_ids(nx.s, nx.c, nx.cb));
-          load(nx.h, nx.c, nx.cb, ids);
-          load_scales(nx.h);
-        }
       }
       un = nx;
       have = have2;
