@@ -89,7 +89,7 @@ def store(pool, scales, new, table, ctx, q_start, block_size) -> None:
                 if now > 0:
                     pool[phys, a:z, h] = encode(v / now)
                 else:
-                    pool[phys, a:z, h] = encode(np.where(np.isinf(v), v, v * 0.0))
+                    pool[phys, a:z, h] = encode(np.where(np.isfinite(v), 0.0 * np.where(np.isfinite(v), v, 0), v))
                 scales[phys, h] = now
 
 

@@ -640,6 +640,21 @@ def test_prefill_long_context_is_cut_into_pieces(mt, dt, h, g, d, n):
     compare(out[rows], lse[rows], want[rows], want_lse[rows], dt)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("order", [1, -1])
+def test_prefill_pieces_of_long_and_short_sequences(mt, dt, order):
+    # the long one's pieces set how many every unit is cut into; most pieces of the
+    # short ones have no chunk
+    ctx = ([6000] + [9 + 11 * s for s in range(9)])[::order]
+    w = World(mt, 57, ctx, 8, 64, 16)
+    cache = w.upload()
+    n = [3] * 10
+    q, qd = w.q(30, 1, dt)
+    out, lse = run_prefill(w, cache, qd, starts(n), dt)
+    want, want_lse = oracle(w, q, q_start=starts(n))
+    compare(out, lse, want, want_lse, dt)
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefill_many_units_a_cta(mt, dt, d):
