@@ -972,11 +972,16 @@ mt_status make_plan(const mt_f8_attn_args *a, const char *where, Plan *pl) {
                    1024;
   p.stages = std::min(kMaxStages, ring / (p.slices * p.stage_bytes));
   const long long rows = (long long)p.B * p.n_hg;
-  // a (sequence, head group) of up to 256 positions is one CTA's work: no
-  // pieces and no second launch
-  p.whole = (long long)p.max_blocks * c.block_size <= 256 && rows <= 0x7fffffffLL;
-  const int per_sm = c.head_dim == 256 ? 1 : 2;
-  pl->ctas = p.whole ? rows : (long long)per_sm * di.n_sm;
+  // One CTA for each (sequence, head group), without pieces and a second launch, when
+  // that is a few steps a warp (2 sequences of 100 positions, 2 steps a warp: 5.7 us
+  // for 6.9; 250 positions, 16 steps a warp: 21.8 for 11.9), or when there are CTAs
+  // enough and steps not too many (256 sequences of 8 heads: 250 positions 30 us for
+  // 38, 500 52 for 57, 1000 96 for 92; 64 sequences of 250: 22.5 for 17.0).
+  const long long grid = (long long)(c.head_dim == 256 ? 1 : 2) * di.n_sm;
+  const long long steps = ((long long)p.max_blocks * c.block_size + kStep - 1) / kStep;
+  p.whole = rows <= 0x7fffffffLL &&
+            (steps <= 6 * p.slices || (steps <= 32 && 4 * rows >= 3 * grid));
+  pl->ctas = p.whole ? rows : grid;
   p.n_ctas = (int)pl->ctas;
   pl->slots = p.whole ? 0 : pl->ctas + rows;
   pl->ws = kHdrBytes + (size_t)pl->slots * p.hc * p.G * (c.head_dim + 2) * sizeof(float);

@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(kThreads, DT == MT_F32 ? 2 : 4)
   auto first_slot = [](int t, int q) { return max(q, 0) / BS + 2 * t; };
   int s, q0, q1, c;
   if (p.n_seqs <= 32) {
-    // a lane has each sequence's first row and length: one round trip
+    // a lane has each sequence's first row and length: one round trip (by the search,
+    // which takes three, a step of 32 sequences 2.8 us for 2.4)
     const int t = min(lane, p.n_seqs - 1);
     const int q_l = p.q_start[t], c_l = p.ctx[t], q_end = p.q_start[p.n_seqs];
     s = 31 - __clz(__ballot_sync(kAll, lane < p.n_seqs && first_slot(t, q_l) <= slot) | 1u);
